@@ -73,6 +73,9 @@ typedef enum { MOE_W_BF16 = 0, MOE_W_INT8 = 1, MOE_W_INT4 = 2 } moe_wfmt;
  * below that (measured crossovers on B200 at the Gemma shape, top-8). */
 typedef enum { MOE_FFN_AUTO = 0, MOE_FFN_GEMV = 1, MOE_FFN_TC = 2 } moe_ffn_path;
 
+/* Scores of moe_route_scored. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
 /*
  * One MoE layer's experts (host struct; the pointers in it are device memory).
  * Expert e is read from   pool + slot_table[e] * expert_bytes   when
@@ -135,6 +138,34 @@ MOE_API moe_status moe_blob_offsets(int32_t fmt, int32_t H, int32_t I, uint64_t 
  */
 MOE_API moe_status moe_route_topk(const float *logits, int32_t T, int32_t E, int32_t k, int32_t *ids, float *w,
                           moe_stream_t stream);
+
+/*
+ * Scored routing.  logits fp32 [T][E], bias fp32 [E] (nullable) -> ids int32
+ * [T][k], w fp32 [T][k]:
+ *   s_e = exp(l_e - max l) / sum exp(l - max l)   (MOE_SCORE_SOFTMAX), or
+ *   s_e = 1 / (1 + exp(-l_e))                     (MOE_SCORE_SIGMOID)
+ *   c_e = s_e + bias_e         chooses (a bias that balances the experts' load);
+ *                              the weight is taken from s
+ *   groups (n_group > 1): experts [g E/n_group, (g+1) E/n_group) are group g, its
+ *   score the sum of its group_top (1 or 2) best c; only the experts of the
+ *   topk_group best groups can win
+ *   ids: the k best c in descending order; w_j = s_j, divided by the sum of the
+ *   token's k scores with renorm != 0 (weights 0 where that sum is 0), times scale.
+ * Equal choices go to the lower expert id, equal groups to the lower group.
+ * Scores and choices are formed and compared in 64 bits, and a weight is rounded
+ * once, to fp32.
+ * Masked experts: one whose logit or bias is not above the lowest finite fp32
+ * (NaN, -inf, -FLT_MAX) is never taken; by its logit it has score 0 and no part in
+ * the softmax.  A group's score is that of its live experts, and a group without
+ * one is never chosen.  A token left with fewer than k experts gets id -1 and
+ * weight 0 in the places that remain (moe_permute leaves those routes out, as it
+ * does those that moe_route_min_weight drops).
+ * E a multiple of n_group; n_group <= 32; 1 <= topk_group <= n_group; k <=
+ * topk_group * E / n_group; group_top <= E / n_group.  One warp per token.
+ */
+MOE_API moe_status moe_route_scored(const float *logits, const float *bias, int32_t T, int32_t E, int32_t k,
+                                    int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                                    int32_t renorm, float scale, int32_t *ids, float *w, moe_stream_t stream);
 
 /*
  * The step before the path, fused with it: the fp32 router projection (prain
@@ -290,6 +321,77 @@ MOE_API moe_status moe_grouped_ffn_noalloc(const moe_layer *layer, const uint16_
  */
 MOE_API moe_status moe_combine(const float *rows, const int32_t *route_pos, const float *w, int32_t T, int32_t k,
                        int32_t H, uint16_t *y, moe_stream_t stream);
+
+/*
+ * Matrix product of int8 codes with a scale per token and per output channel:
+ *   y[t][n] = sx[t] * sw[n] * sum_k xq[t][k] * wq[n][k]
+ * xq int8 [T][K], sx fp32 [T] (a token's codes: moe_norm, or moe_quantize_int8 of
+ * its row); wq int8 [N][K], sw fp32 [N] (moe_quantize_int8 of the weight); y bf16
+ * [T][N], or fp32 [T][N] with out_fp32 != 0.  The sum is exact (int32; codes may
+ * be -128), so a result carries the rounding of the scales' products and of its own type
+ * only, and it is the same whatever kernel a shape takes.  K a multiple of 16 in [16, 65536]; N >= 1;
+ * xq, wq and y 16-byte aligned.
+ */
+MOE_API moe_status moe_linear_int8(const int8_t *xq, const float *sx, const int8_t *wq, const float *sw, int32_t T,
+                                   int32_t N, int32_t K, void *y, int32_t out_fp32, moe_stream_t stream);
+
+/*
+ * The grouped FFN with int8 activations, over a layer of int8 experts (fmt
+ * MOE_W_INT8; MOE_ERR_UNSUPPORTED otherwise): moe_grouped_ffn with the codes of
+ * both matrices multiplied as they are.  xq int8 [T][H] and sx fp32 [T] are the
+ * tokens' codes and scales; counts, offsets and sorted_route from moe_permute.  For
+ * every sorted row s < offsets[E] of expert e with token t = sorted_route[s] / k:
+ *   g = s13 sx[t] (Q13_e xq[t]);  h_i = gelu_tanh(g_i) * g_{I+i}       (fp32)
+ *   sh = max |h| / 127;  hq = clamp(rint(h / sh), -127, 127)           (per row)
+ *   rows[s] = s2 sh (Q2_e hq)
+ * with exact integer sums, fp32 elsewhere.  h is quantised from its fp32 value, a
+ * scale per row, so that its codes do not depend on a rounding in between.  rows fp32 [T*k][H] in
+ * sorted order for moe_combine or moe_combine_norm; rows past offsets[E] are not
+ * written.  ws: at least moe_grouped_ffn_w8a8_workspace() bytes, 16-byte aligned;
+ * calls that overlap on the GPU need a workspace each.  Slot tables as in
+ * moe_grouped_ffn, a slot past the pool included.
+ */
+MOE_API size_t moe_grouped_ffn_w8a8_workspace(const moe_layer *layer, int32_t T, int32_t k);
+MOE_API moe_status moe_grouped_ffn_w8a8(const moe_layer *layer, const int8_t *xq, const float *sx, int32_t T,
+                                        int32_t k, const int32_t *counts, const int32_t *offsets,
+                                        const int32_t *sorted_route, float *rows, void *ws, size_t ws_bytes,
+                                        moe_stream_t stream);
+
+/*
+ * The norms around a block.  moe_norm is the norm before one:
+ *   n  = x[t] * rsqrt(mean(x[t]^2) + eps) * (offset + weight)          (fp32)
+ *   xn = n rounded to bf16;   sx = max |n| / 127,  xq = rint(n / sx)   (codes)
+ * x bf16 [T][H], weight bf16 [H]; xn bf16 [T][H] and xq int8 [T][H] with sx fp32
+ * [T] are outputs, either of the two nullable (xq and sx go together).  The codes
+ * are those of n before its rounding to bf16; a row of zeros has scale 0, and a
+ * NaN takes no part in the maximum and has code 0.
+ *
+ * moe_residual_norm and moe_combine_norm are what follows a block: its output z
+ * is normalised, gated and added to the residual, and the sum is normalised for
+ * the next block, in one launch:
+ *   z[t]  the block's output, bf16 [T][H]   (moe_residual_norm), or
+ *   z[t]  = sum_{j<k} w[t][j] * rows[route_pos[t*k+j]], in fp32 and not rounded
+ *           (moe_combine_norm; rows, route_pos and w as in moe_combine: a route
+ *           whose position is outside [0, T*k) contributes nothing)
+ *   zn    = z * rsqrt(mean(z^2) + eps) * (offset + post_w)   (z without post_w)
+ *   y[t]  = residual_scale * residual[t] + block_scale * gate_t[t] * gate_h * zn
+ *   xn, xq, sx = moe_norm's of y[t] as stored, with next_w (none without next_w)
+ * residual bf16 [T][H]; post_w, next_w bf16 [H], gate_h fp32 [H] and gate_t fp32
+ * [T] nullable; y bf16 [T][H] may be residual or z itself.  Means and sums are
+ * fp32.  eps > 0; H a multiple of 64 in [64, 16384]; 16-byte aligned pointers
+ * (sx, gate_t, route_pos and w: 4).
+ */
+MOE_API moe_status moe_norm(const uint16_t *x, const uint16_t *weight, int32_t T, int32_t H, float eps, float offset,
+                            uint16_t *xn, int8_t *xq, float *sx, moe_stream_t stream);
+MOE_API moe_status moe_residual_norm(const uint16_t *z, const uint16_t *residual, const uint16_t *post_w,
+                                     const float *gate_h, const float *gate_t, const uint16_t *next_w, int32_t T,
+                                     int32_t H, float eps, float offset, float residual_scale, float block_scale,
+                                     uint16_t *y, uint16_t *xn, int8_t *xq, float *sx, moe_stream_t stream);
+MOE_API moe_status moe_combine_norm(const float *rows, const int32_t *route_pos, const float *w, int32_t k,
+                                    const uint16_t *residual, const uint16_t *post_w, const float *gate_h,
+                                    const float *gate_t, const uint16_t *next_w, int32_t T, int32_t H, float eps,
+                                    float offset, float residual_scale, float block_scale, uint16_t *y, uint16_t *xn,
+                                    int8_t *xq, float *sx, moe_stream_t stream);
 
 /*
  * The whole layer in one call: route -> permute (+hits) -> grouped FFN ->

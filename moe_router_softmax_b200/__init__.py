@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import numpy as np
 import torch
@@ -28,6 +29,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_TIMEOUT = range(5)
 MOE_W_BF16, MOE_W_INT8, MOE_W_INT4 = 0, 1, 2
 MOE_FFN_AUTO, MOE_FFN_GEMV, MOE_FFN_TC = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 FMT = {"bf16": MOE_W_BF16, "int8": MOE_W_INT8, "int4": MOE_W_INT4}
 
 # every symbol include/moe.h declares
@@ -40,6 +42,8 @@ EXPORTS = [
     "moe_should_refresh", "moe_budget_from_vram", "moe_grouped_ffn_noalloc", "moe_take_device_errors",
     "moe_route_min_weight", "moe_router_topk", "moe_hits_window", "moe_refresh_device", "moe_promote_copies",
     "moe_gather_rows", "moe_ep_recv_ids", "moe_ep_splits",
+    "moe_route_scored", "moe_linear_int8", "moe_grouped_ffn_w8a8_workspace", "moe_grouped_ffn_w8a8", "moe_norm",
+    "moe_residual_norm", "moe_combine_norm",
 ]
 
 
@@ -58,6 +62,7 @@ class _CLayer(ctypes.Structure):
 
 
 P, i32, i64, u64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
+f32 = ctypes.c_float
 LP = ctypes.POINTER(_CLayer)
 _SIG = {
     "moe_version": (ctypes.c_char_p, []),
@@ -93,6 +98,13 @@ _SIG = {
     "moe_gather_rows": (i32, [P, i32, i32, P, i32, i32, P, P]),
     "moe_ep_recv_ids": (i32, [P, i32, i32, P, i32, P]),
     "moe_ep_splits": (i32, [P, i32, P, i32, P, P]),
+    "moe_route_scored": (i32, [P, P, i32, i32, i32, i32, i32, i32, i32, i32, f32, P, P, P]),
+    "moe_linear_int8": (i32, [P, P, P, P, i32, i32, i32, P, i32, P]),
+    "moe_grouped_ffn_w8a8_workspace": (sz, [LP, i32, i32]),
+    "moe_grouped_ffn_w8a8": (i32, [LP, P, P, i32, i32, P, P, P, P, P, sz, P]),
+    "moe_norm": (i32, [P, P, i32, i32, f32, f32, P, P, P, P]),
+    "moe_residual_norm": (i32, [P, P, P, P, P, P, i32, i32, f32, f32, f32, f32, P, P, P, P, P]),
+    "moe_combine_norm": (i32, [P, P, P, i32, P, P, P, P, P, i32, i32, f32, f32, f32, f32, P, P, P, P, P]),
 }
 for _name, (_res, _args) in _SIG.items():
     _f = getattr(_lib, _name)
@@ -510,6 +522,187 @@ def moe_ep_splits(counts: np.ndarray, recv_counts: np.ndarray):
     _check(_lib.moe_ep_splits(pc, c.size, pr, N, send.ctypes.data_as(ctypes.c_void_p),
                               recv.ctypes.data_as(ctypes.c_void_p)))
     return send, recv
+
+
+# ------------------------------------------- operators around int8 experts
+# Their arguments are checked against one another as well (shapes, one device),
+# and a call runs on its tensors' device whatever the current one is.
+
+def _arg(t, shape, dtype, name: str, dev):
+    """Device address of a tensor argument, or None for None."""
+    if t is None:
+        return None
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device_of(t: torch.Tensor, ndim: int, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions")
+    return t.device
+
+
+def _call(fn, dev, stream, *args) -> None:
+    """Run an entry point on `dev`, on `stream` or the device's current stream."""
+    idx = dev.index
+    if idx == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(idx):
+            st = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
+    if st != MOE_OK:
+        _check(st)
+
+
+def moe_route_scored(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, score: int = MOE_SCORE_SOFTMAX,
+                     n_group: int = 1, topk_group: int = 1, group_top: int = 1, renorm: bool = True,
+                     scale: float = 1.0, ids: torch.Tensor | None = None, w: torch.Tensor | None = None, stream=None):
+    """Routing by softmax or sigmoid scores, a bias in the choice, expert groups
+    and (re)normalised weights; masked experts (see include/moe.h).  Returns (ids, w):
+    int32 [T, k] (-1 where a token has fewer than k live experts) and fp32 [T, k]."""
+    dev = _device_of(logits, 2, "logits")
+    T, E = logits.shape
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev) if ids is None else ids
+    w = torch.empty((T, k), dtype=torch.float32, device=dev) if w is None else w
+    _call(_lib.moe_route_scored, dev, stream, _arg(logits, (T, E), torch.float32, "logits", dev),
+          _arg(bias, (E,), torch.float32, "bias", dev), T, E, k, score, n_group, topk_group, group_top, bool(renorm),
+          scale, _arg(ids, (T, k), torch.int32, "ids", dev), _arg(w, (T, k), torch.float32, "w", dev))
+    return ids, w
+
+
+def moe_linear_int8(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
+                    dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[t, n] = sx[t] * sw[n] * (xq[t] . wq[n]) over int8 codes xq [T, K], wq [N, K];
+    y bf16 or fp32 [T, N] (``dtype``, or that of ``y``)."""
+    dev = _device_of(xq, 2, "xq")
+    T, K = xq.shape
+    N = wq.shape[0]
+    if y is None:
+        y = torch.empty((T, N), dtype=dtype, device=dev)
+    _call(_lib.moe_linear_int8, dev, stream, _arg(xq, (T, K), torch.int8, "xq", dev),
+          _arg(sx, (T,), torch.float32, "sx", dev), _arg(wq, (N, K), torch.int8, "wq", dev),
+          _arg(sw, (N,), torch.float32, "sw", dev), T, N, K,
+          _arg(y, (T, N), (torch.bfloat16, torch.float32), "y", dev), y.dtype is torch.float32)
+    return y
+
+
+def moe_grouped_ffn_w8a8_workspace(layer: MoeLayer, T: int, k: int) -> int:
+    return int(_lib.moe_grouped_ffn_w8a8_workspace(layer.ref(), T, k))
+
+
+def moe_grouped_ffn_w8a8(layer: MoeLayer, xq: torch.Tensor, sx: torch.Tensor, k: int, counts: torch.Tensor,
+                         offsets: torch.Tensor, sorted_route: torch.Tensor, rows: torch.Tensor | None = None,
+                         ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The grouped FFN of an int8 layer with int8 activations (codes xq [T, H],
+    scales sx [T], as moe_norm or moe_quantize_int8 make them): fp32 rows
+    [T*k, H] in sorted order, for moe_combine or moe_combine_norm."""
+    dev = _device_of(xq, 2, "xq")
+    if layer.home.device != dev:
+        raise ValueError(f"the layer is on {layer.home.device}, xq on {dev}")
+    T, R = xq.shape[0], xq.shape[0] * k
+    if rows is None:
+        rows = torch.empty((R, layer.H), dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = torch.empty(max(moe_grouped_ffn_w8a8_workspace(layer, T, k), 16), dtype=torch.uint8, device=dev)
+    _call(_lib.moe_grouped_ffn_w8a8, dev, stream, layer.ref(), _arg(xq, (T, layer.H), torch.int8, "xq", dev),
+          _arg(sx, (T,), torch.float32, "sx", dev), T, k, _arg(counts, (layer.E,), torch.int32, "counts", dev),
+          _arg(offsets, (layer.E + 1,), torch.int32, "offsets", dev),
+          _arg(sorted_route, (R,), torch.int32, "sorted_route", dev),
+          _arg(rows, (R, layer.H), torch.float32, "rows", dev), _arg(ws, ws.shape, torch.uint8, "ws", dev), ws.numel())
+    return rows
+
+
+class NormOut(NamedTuple):
+    """Outputs of the block norms; None where not asked for."""
+    y: Optional[torch.Tensor]   # bf16 [T, H], the new residual
+    xn: Optional[torch.Tensor]  # bf16 [T, H], normalised for the next block
+    xq: Optional[torch.Tensor]  # int8 [T, H], its codes
+    sx: Optional[torch.Tensor]  # fp32 [T], their scales
+
+
+def _norm_out(T, H, dev, y, xn, xq, sx, want_xn, codes) -> NormOut:
+    if xn is None and want_xn:
+        xn = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if codes:
+        xq = torch.empty((T, H), dtype=torch.int8, device=dev) if xq is None else xq
+        sx = torch.empty((T,), dtype=torch.float32, device=dev) if sx is None else sx
+    return NormOut(y, xn, xq, sx)
+
+
+def moe_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: float = 0.0, codes: bool = False,
+             want_xn: bool = True, xn: torch.Tensor | None = None, xq: torch.Tensor | None = None,
+             sx: torch.Tensor | None = None, stream=None) -> NormOut:
+    """The norm before a block: x * rsqrt(mean(x^2) + eps) * (offset + weight) as bf16
+    (``want_xn``) and, with ``codes``, as int8 codes with a scale per token."""
+    dev = _device_of(x, 2, "x")
+    T, H = x.shape
+    o = _norm_out(T, H, dev, None, xn, xq, sx, want_xn, codes)
+    bf = torch.bfloat16
+    _call(_lib.moe_norm, dev, stream, _arg(x, (T, H), bf, "x", dev), _arg(weight, (H,), bf, "weight", dev), T, H, eps,
+          offset, _arg(o.xn, (T, H), bf, "xn", dev), _arg(o.xq, (T, H), torch.int8, "xq", dev),
+          _arg(o.sx, (T,), torch.float32, "sx", dev))
+    return o
+
+
+def _after_block(fn, src, residual, post_weight, gate_h, gate_t, next_weight, eps, offset, residual_scale, block_scale,
+                 codes, want_xn, y, xn, xq, sx, stream) -> NormOut:
+    dev = _device_of(residual, 2, "residual")
+    T, H = residual.shape
+    bf, fp = torch.bfloat16, torch.float32
+    y = torch.empty((T, H), dtype=bf, device=dev) if y is None else y
+    has_next = next_weight is not None
+    o = _norm_out(T, H, dev, y, xn, xq, sx, want_xn and has_next, codes)
+    _call(fn, dev, stream, *src(T, H, dev), _arg(residual, (T, H), bf, "residual", dev),
+          _arg(post_weight, (H,), bf, "post_weight", dev), _arg(gate_h, (H,), fp, "gate_h", dev),
+          _arg(gate_t, (T,), fp, "gate_t", dev), _arg(next_weight, (H,), bf, "next_weight", dev), T, H, eps, offset,
+          residual_scale, block_scale, _arg(y, (T, H), bf, "y", dev), _arg(o.xn, (T, H), bf, "xn", dev),
+          _arg(o.xq, (T, H), torch.int8, "xq", dev), _arg(o.sx, (T,), fp, "sx", dev))
+    return o
+
+
+def moe_residual_norm(z: torch.Tensor, residual: torch.Tensor, post_weight: torch.Tensor | None = None,
+                      gate_h: torch.Tensor | None = None, gate_t: torch.Tensor | None = None,
+                      next_weight: torch.Tensor | None = None, eps: float = 1e-6, offset: float = 0.0,
+                      residual_scale: float = 1.0, block_scale: float = 1.0, codes: bool = False, want_xn: bool = True,
+                      y: torch.Tensor | None = None, xn: torch.Tensor | None = None, xq: torch.Tensor | None = None,
+                      sx: torch.Tensor | None = None, stream=None) -> NormOut:
+    """After a dense block: y = residual_scale * residual + block_scale * gate_t *
+    gate_h * norm(z), and y normalised for the next block (``next_weight``) as bf16
+    and, with ``codes``, as int8 codes."""
+    def src(T, H, dev):
+        return (_arg(z, (T, H), torch.bfloat16, "z", dev),)
+
+    return _after_block(_lib.moe_residual_norm, src, residual, post_weight, gate_h, gate_t, next_weight, eps, offset,
+                        residual_scale, block_scale, codes, want_xn, y, xn, xq, sx, stream)
+
+
+def moe_combine_norm(rows: torch.Tensor, route_pos: torch.Tensor, w: torch.Tensor, residual: torch.Tensor,
+                     post_weight: torch.Tensor | None = None, gate_h: torch.Tensor | None = None,
+                     gate_t: torch.Tensor | None = None, next_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                     offset: float = 0.0, residual_scale: float = 1.0, block_scale: float = 1.0, codes: bool = False,
+                     want_xn: bool = True, y: torch.Tensor | None = None, xn: torch.Tensor | None = None,
+                     xq: torch.Tensor | None = None, sx: torch.Tensor | None = None, stream=None) -> NormOut:
+    """After the experts: moe_residual_norm of the combined rows (moe_combine's sum,
+    kept in fp32); rows fp32 [T*k, H], route_pos int32 [T*k], w fp32 [T, k]."""
+    if w.dim() != 2:
+        raise ValueError("w must have 2 dimensions")
+    k = w.shape[1]
+
+    def src(T, H, dev):
+        return (_arg(rows, (T * k, H), torch.float32, "rows", dev),
+                _arg(route_pos, (T * k,), torch.int32, "route_pos", dev), _arg(w, (T, k), torch.float32, "w", dev), k)
+
+    return _after_block(_lib.moe_combine_norm, src, residual, post_weight, gate_h, gate_t, next_weight, eps, offset,
+                        residual_scale, block_scale, codes, want_xn, y, xn, xq, sx, stream)
 
 
 # ------------------------------------------------------------------ helpers

@@ -4,7 +4,7 @@
 #include <stdio.h>
 #include <string.h>
 
-#include "common.cuh"
+#include "ops.cuh"
 
 namespace moe {
 
@@ -151,6 +151,28 @@ moe_status moe_route_topk(const float *logits, int32_t T, int32_t E, int32_t k, 
     if (T == 0) return MOE_OK;
     CHECK_ARG(logits && ids && w, "moe_route_topk: NULL pointer");
     return cuda_status(launch_route_topk(logits, T, E, k, ids, w, (cudaStream_t)stream), "moe_route_topk launch");
+}
+
+moe_status moe_route_scored(const float *logits, const float *bias, int32_t T, int32_t E, int32_t k, int32_t score,
+                            int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renorm, float scale,
+                            int32_t *ids, float *w, moe_stream_t stream) {
+    moe_status st = check_shape(E, k, 64, 64);
+    if (st != MOE_OK) return st;
+    if ((st = check_tk(T, k)) != MOE_OK) return st;
+    CHECK_ARG(score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID, "unknown score %d", score);
+    CHECK_ARG(n_group >= 1 && n_group <= 32 && E % n_group == 0, "n_group=%d must divide E=%d and lie in [1, 32]",
+              n_group, E);
+    CHECK_ARG(topk_group >= 1 && topk_group <= n_group, "topk_group=%d outside [1, n_group=%d]", topk_group, n_group);
+    CHECK_ARG(k <= topk_group * (E / n_group), "k=%d exceeds the %d experts of %d groups", k,
+              topk_group * (E / n_group), topk_group);
+    CHECK_ARG(group_top >= 1 && group_top <= 2 && group_top <= E / n_group,
+              "group_top=%d must be 1 or 2 and at most E/n_group=%d", group_top, E / n_group);
+    CHECK_ARG(scale - scale == 0.0f, "scale is not finite");
+    if (T == 0) return MOE_OK;
+    CHECK_ARG(logits && ids && w, "moe_route_scored: NULL pointer");
+    const ScoredArgs a{logits, bias, T, E, k, score == MOE_SCORE_SIGMOID, n_group, E / n_group, topk_group, group_top,
+                       renorm != 0, scale, ids, w};
+    return cuda_status(launch_route_scored(a, (cudaStream_t)stream), "moe_route_scored launch");
 }
 
 moe_status moe_router_topk(const uint16_t *x, const float *w_router, int32_t T, int32_t H, int32_t E, int32_t k,
@@ -392,6 +414,103 @@ moe_status moe_layer_forward(const moe_layer *layer, const float *logits, const 
     return moe_combine(rows, pos, w, T, k, v.H, y, stream);
 }
 
+moe_status moe_linear_int8(const int8_t *xq, const float *sx, const int8_t *wq, const float *sw, int32_t T, int32_t N,
+                           int32_t K, void *y, int32_t out_fp32, moe_stream_t stream) {
+    CHECK_ARG(T >= 0, "T=%d is negative", T);
+    CHECK_ARG(N >= 1, "N=%d must be positive", N);
+    CHECK_ARG(K >= 16 && K <= 65536 && K % 16 == 0, "K=%d must be a multiple of 16 in [16, 65536]", K);
+    if (T == 0) return MOE_OK;
+    CHECK_ARG(xq && sx && wq && sw && y, "moe_linear_int8: NULL pointer");
+    CHECK_ARG(aligned16(xq) && aligned16(wq) && aligned16(y), "xq, wq and y must be 16-byte aligned");
+    const LinearArgs a{xq, wq, sx, sw, T, N, K, y, out_fp32 != 0};
+    return cuda_status(launch_linear_i8(a, (cudaStream_t)stream), "moe_linear_int8 launch");
+}
+
+size_t moe_grouped_ffn_w8a8_workspace(const moe_layer *layer, int32_t T, int32_t k) {
+    if (!layer || T < 0 || k < 1) return 0;
+    return align256(ffn_i8_workspace(layer->E, layer->H, layer->I, T, k));
+}
+
+moe_status moe_grouped_ffn_w8a8(const moe_layer *layer, const int8_t *xq, const float *sx, int32_t T, int32_t k,
+                                const int32_t *counts, const int32_t *offsets, const int32_t *sorted_route, float *rows,
+                                void *ws, size_t ws_bytes, moe_stream_t stream) {
+    LayerView v;
+    moe_status st = layer_view(layer, &v);
+    if (st != MOE_OK) return st;
+    if (v.fmt != MOE_W_INT8)
+        return set_error(MOE_ERR_UNSUPPORTED, "moe_grouped_ffn_w8a8 takes int8 experts, not format %d", v.fmt);
+    if ((st = check_shape(v.E, k, v.H, v.I)) != MOE_OK) return st;
+    if ((st = check_tk(T, k)) != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    CHECK_ARG(xq && sx && counts && offsets && sorted_route && rows && ws, "moe_grouped_ffn_w8a8: NULL pointer");
+    CHECK_ARG(aligned16(xq) && aligned16(rows) && aligned16(ws), "xq, rows and ws must be 16-byte aligned");
+    const size_t need = align256(ffn_i8_workspace(v.E, v.H, v.I, T, k));
+    CHECK_ARG(ws_bytes >= need, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    const FfnI8Args a{v, xq, sx, T, k, counts, offsets, sorted_route, rows, ws};
+    return cuda_status(launch_ffn_i8(a, (cudaStream_t)stream), "moe_grouped_ffn_w8a8 launch");
+}
+
+// Checks shared by the block norms (T > 0), then the launch.
+static moe_status block_norm(const NormArgs &a, bool block, const char *what, moe_stream_t stream) {
+    CHECK_ARG(a.T >= 0, "T=%d is negative", a.T);
+    CHECK_ARG(a.H >= 64 && a.H <= 16384 && a.H % 64 == 0, "H=%d must be a multiple of 64 in [64, 16384]", a.H);
+    CHECK_ARG(a.eps > 0.0f && a.eps - a.eps == 0.0f, "eps=%g must be positive and finite", a.eps);
+    CHECK_ARG(a.offset - a.offset == 0.0f && a.residual_scale - a.residual_scale == 0.0f &&
+                  a.block_scale - a.block_scale == 0.0f,
+              "offset, residual_scale and block_scale must be finite");
+    if (a.T == 0) return MOE_OK;
+    CHECK_ARG((a.xq == nullptr) == (a.sx == nullptr), "%s: xq and sx go together", what);
+    CHECK_ARG(a.next_w != nullptr || (a.xn == nullptr && a.xq == nullptr), "%s: xn and xq need the next norm's weight",
+              what);
+    CHECK_ARG(block || a.xn != nullptr || a.xq != nullptr, "%s: neither xn nor xq given", what);
+    CHECK_ARG(!block || a.next_w == nullptr || a.xn != nullptr || a.xq != nullptr,
+              "%s: a next norm without an output", what);
+    CHECK_ARG(a.residual && (!block || a.y), "%s: NULL pointer", what);
+    CHECK_ARG(aligned16(a.rows) && aligned16(a.z) && aligned16(a.residual) && aligned16(a.post_w) &&
+                  aligned16(a.next_w) && aligned16(a.gate_h) && aligned16(a.y) && aligned16(a.xn) && aligned16(a.xq),
+              "%s: matrices, norm weights and gate_h must be 16-byte aligned", what);
+    return cuda_status(launch_block_norm(a, (cudaStream_t)stream), what);
+}
+
+moe_status moe_norm(const uint16_t *x, const uint16_t *weight, int32_t T, int32_t H, float eps, float offset,
+                    uint16_t *xn, int8_t *xq, float *sx, moe_stream_t stream) {
+    CHECK_ARG(T <= 0 || weight, "moe_norm: NULL pointer");
+    NormArgs a{};
+    a.residual = x;
+    a.next_w = weight;
+    a.eps = eps;
+    a.offset = offset;
+    a.T = T;
+    a.H = H;
+    a.xn = xn;
+    a.xq = xq;
+    a.sx = sx;
+    return block_norm(a, false, "moe_norm", stream);
+}
+
+moe_status moe_residual_norm(const uint16_t *z, const uint16_t *residual, const uint16_t *post_w, const float *gate_h,
+                             const float *gate_t, const uint16_t *next_w, int32_t T, int32_t H, float eps, float offset,
+                             float residual_scale, float block_scale, uint16_t *y, uint16_t *xn, int8_t *xq, float *sx,
+                             moe_stream_t stream) {
+    CHECK_ARG(T <= 0 || z, "moe_residual_norm: NULL pointer");
+    const NormArgs a{nullptr, nullptr, nullptr, 0, z, residual, post_w, next_w, gate_h, gate_t, eps, offset,
+                     residual_scale, block_scale, T, H, y, xn, xq, sx};
+    return block_norm(a, true, "moe_residual_norm", stream);
+}
+
+moe_status moe_combine_norm(const float *rows, const int32_t *route_pos, const float *w, int32_t k,
+                            const uint16_t *residual, const uint16_t *post_w, const float *gate_h, const float *gate_t,
+                            const uint16_t *next_w, int32_t T, int32_t H, float eps, float offset, float residual_scale,
+                            float block_scale, uint16_t *y, uint16_t *xn, int8_t *xq, float *sx, moe_stream_t stream) {
+    CHECK_ARG(k >= 1 && k <= kMaxK, "k=%d outside [1, %d]", k, kMaxK);
+    moe_status st = check_tk(T, k);
+    if (st != MOE_OK) return st;
+    CHECK_ARG(T == 0 || (rows && route_pos && w), "moe_combine_norm: NULL pointer");
+    const NormArgs a{rows, route_pos, w, k, nullptr, residual, post_w, next_w, gate_h, gate_t, eps, offset,
+                     residual_scale, block_scale, T, H, y, xn, xq, sx};
+    return block_norm(a, true, "moe_combine_norm", stream);
+}
+
 moe_status moe_quantize_int8(const uint16_t *w, int32_t rows, int32_t K, int8_t *q, float *scale, moe_stream_t stream) {
     CHECK_ARG(rows >= 0 && K >= 1, "rows=%d K=%d", rows, K);
     if (rows == 0) return MOE_OK;
@@ -428,13 +547,14 @@ moe_status moe_take_device_errors(uint32_t *code, uint32_t *info) {
     CHECK_ARG(code && info, "moe_take_device_errors: NULL pointer");
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_status(e, "moe_take_device_errors: device synchronise");
-    unsigned c = 0, i = 0, cg = 0, ig = 0;
+    unsigned c = 0, i = 0, cg = 0, ig = 0, c8 = 0, i8 = 0;
     e = tc_take_error(&c, &i);
     if (e == cudaSuccess) e = gemv_take_error(&cg, &ig);
+    if (e == cudaSuccess) e = i8_take_error(&c8, &i8);
     if (e != cudaSuccess) return cuda_status(e, "moe_take_device_errors: read");
-    if (c == 0) {  // the tensor-core word first, then the GEMV kernels' word
-        c = cg;
-        i = ig;
+    if (c == 0) {  // the tensor-core word first, then the GEMV kernels' word, then the int8-activation kernels'
+        c = cg ? cg : c8;
+        i = cg ? ig : i8;
     }
     *code = c;
     *info = i;

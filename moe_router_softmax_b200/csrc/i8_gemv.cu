@@ -1,0 +1,197 @@
+// i8_gemv.cu -- int8 x int8 products for few tokens: dot products of codes with
+// dp4a (four multiply-adds per lane and instruction, int32 sums, exact), the
+// scales applied once per output.
+//
+//   linear  y[t][n] = sx[t] sw[n] sum_k xq[t][k] wq[n][k]
+//   ffn     g = s13 sx (Q13 xq);  h_i = gelu_tanh(g_i) g_{I+i}   (fp32)
+//           sh = max |h| / 127,  hq = rint(h / sh);  rows = s2 sh (Q2 hq)
+//
+// A weight row is read once, 16 bytes per lane, so the weights' bytes bound
+// these kernels.
+#include "ops.cuh"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kWarps = 4;
+
+// First problem a kernel of this file recorded (0 = none), read and cleared by
+// moe_take_device_errors(): 0x2005 a slot past the pool, 0x2007 a route out of range.
+__device__ unsigned int g_i8_error;
+__device__ unsigned int g_i8_error_info;
+__device__ __forceinline__ void record_error(unsigned code, unsigned info) {
+    if (atomicCAS(&g_i8_error, 0u, code) == 0u) g_i8_error_info = info;
+}
+
+__device__ __forceinline__ int dot16(uint4 w, uint4 x, int acc) {
+    acc = __dp4a((int)w.x, (int)x.x, acc);
+    acc = __dp4a((int)w.y, (int)x.y, acc);
+    acc = __dp4a((int)w.z, (int)x.z, acc);
+    return __dp4a((int)w.w, (int)x.w, acc);
+}
+
+// One warp per output row n and block of TB tokens.
+template <int TB, bool FP32>
+__global__ void __launch_bounds__(32 * kWarps) k_linear_i8(const LinearArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int n = blockIdx.x * kWarps + (threadIdx.x >> 5), t0 = blockIdx.y * TB;
+    if (n >= a.N) return;
+    const int nch = a.K / 16;
+    const uint4 *wr = reinterpret_cast<const uint4 *>(a.wq + (size_t)n * a.K);
+    int acc[TB] = {};
+    for (int c0 = lane; c0 < nch; c0 += 128) {
+        uint4 w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            w[u] = c0 + 32 * u < nch ? ld_stream_v4(wr + c0 + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (c0 + 32 * u < nch)
+#pragma unroll
+                for (int t = 0; t < TB; ++t)
+                    if (t0 + t < a.T)
+                        acc[t] = dot16(w[u],
+                                       __ldg(reinterpret_cast<const uint4 *>(a.xq + (size_t)(t0 + t) * a.K) + c0 + 32 * u),
+                                       acc[t]);
+    }
+    const float sw = __ldg(a.sw + n);
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+        const int sum = __reduce_add_sync(kAll, acc[t]);
+        if (lane != t || t0 + t >= a.T) continue;
+        const float v = (float)sum * __ldg(a.sx + t0 + t) * sw;
+        const size_t at = (size_t)(t0 + t) * a.N + n;
+        if (FP32) static_cast<float *>(a.y)[at] = v;
+        else static_cast<uint16_t *>(a.y)[at] = f32_to_bf16_rne(v);
+    }
+}
+
+// Expert of sorted row s < offsets[E] (the number of experts whose rows end at
+// or before s), by one warp.
+__device__ __forceinline__ int expert_of_row(const int32_t *offsets, int E, int s) {
+    int n = 0;
+    for (int e = threadIdx.x & 31; e < E; e += 32) n += __ldg(offsets + e + 1) <= s;
+    return __reduce_add_sync(kAll, n);
+}
+
+// Phase 1: one warp per sorted row and intermediate column (a gate row and its
+// up row of W13).
+__global__ void __launch_bounds__(32 * kWarps) k_ffn_i8_gemv1(const FfnI8Args a, float *__restrict__ h) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, I = a.L.I, H = a.L.H, per = I / kWarps;
+    const int s = blockIdx.x / per, i = (blockIdx.x % per) * kWarps + (threadIdx.x >> 5);
+    const int R = a.T * a.k;
+    if (s >= min(__ldg(a.offsets + a.L.E), R)) return;
+    const int e = expert_of_row(a.offsets, a.L.E, s);
+    const int route = __ldg(a.sorted_route + s);
+    const uint8_t *blob = e < a.L.E ? expert_blob(a.L, e) : nullptr;
+    if (blob == nullptr || route < 0 || route >= R) {
+        if (lane == 0) {
+            if (e < a.L.E && blob == nullptr) record_error(0x2005u, (unsigned)__ldg(a.L.slot_table + e));
+            else record_error(0x2007u, (unsigned)s);
+        }
+        return;
+    }
+    const int t = route / a.k;
+    const uint4 *wg = reinterpret_cast<const uint4 *>(blob + a.L.off.q13 + (size_t)i * H);
+    const uint4 *wu = reinterpret_cast<const uint4 *>(blob + a.L.off.q13 + (size_t)(I + i) * H);
+    const uint4 *x = reinterpret_cast<const uint4 *>(a.xq + (size_t)t * H);
+    int ag = 0, au = 0;
+#pragma unroll 4
+    for (int c = lane; c < H / 16; c += 32) {
+        const uint4 xv = __ldg(x + c);
+        ag = dot16(ld_stream_v4(wg + c), xv, ag);
+        au = dot16(ld_stream_v4(wu + c), xv, au);
+    }
+    ag = __reduce_add_sync(kAll, ag);
+    au = __reduce_add_sync(kAll, au);
+    if (lane == 0) {
+        const float *s13 = reinterpret_cast<const float *>(blob + a.L.off.s13);
+        const float sx = __ldg(a.sx + t);
+        h[(size_t)s * I + i] = gelu_tanh_f((float)ag * sx * __ldg(s13 + i)) * ((float)au * sx * __ldg(s13 + I + i));
+    }
+}
+
+// Phase 2: a CTA takes 32 output rows of one sorted row; it forms the codes of
+// that row's h in shared memory first.
+constexpr int kRows2 = 32;
+__global__ void __launch_bounds__(32 * kWarps) k_ffn_i8_gemv2(const FfnI8Args a, const float *__restrict__ h) {
+    extern __shared__ __align__(16) int8_t s_hq[];  // [I]
+    __shared__ float s_part[kWarps];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, I = a.L.I, H = a.L.H;
+    const int per = H / kRows2;
+    const int s = blockIdx.x / per, n0 = (blockIdx.x % per) * kRows2;
+    const int R = a.T * a.k;
+    if (s >= min(__ldg(a.offsets + a.L.E), R)) return;
+    const int e = expert_of_row(a.offsets, a.L.E, s);
+    const uint8_t *blob = e < a.L.E ? expert_blob(a.L, e) : nullptr;
+    if (blob == nullptr) return;  // recorded by phase 1
+    const float *hr = h + (size_t)s * I;
+    float amax = 0.0f;
+    for (int i = threadIdx.x; i < I; i += 32 * kWarps) amax = fmaxf(amax, fabsf(hr[i]));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
+    if (lane == 0) s_part[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_part[w]);
+    const float sh = __fdiv_rn(amax, 127.0f);
+    for (int i = threadIdx.x; i < I; i += 32 * kWarps) s_hq[i] = (int8_t)code_i8(hr[i], sh);
+    __syncthreads();
+    const float *s2 = reinterpret_cast<const float *>(blob + a.L.off.s2);
+    for (int n = n0 + warp; n < n0 + kRows2; n += kWarps) {
+        const uint4 *w = reinterpret_cast<const uint4 *>(blob + a.L.off.q2 + (size_t)n * I);
+        int acc = 0;
+        for (int c = lane; c < I / 16; c += 32)
+            acc = dot16(ld_stream_v4(w + c), reinterpret_cast<const uint4 *>(s_hq)[c], acc);
+        acc = __reduce_add_sync(kAll, acc);
+        if (lane == 0) a.rows[(size_t)s * H + n] = (float)acc * sh * __ldg(s2 + n);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_i8(const LinearArgs &a, cudaStream_t s) {
+    if (a.T == 0) return cudaSuccess;
+    const dim3 block(32 * kWarps);
+    auto go = [&](auto kern, int tb) {
+        return launch_pdl(kern, dim3((unsigned)((a.N + kWarps - 1) / kWarps), (unsigned)((a.T + tb - 1) / tb)), block, 0,
+                          s, a);
+    };
+    if (a.T == 1) return a.fp32 ? go(k_linear_i8<1, true>, 1) : go(k_linear_i8<1, false>, 1);
+    return a.fp32 ? go(k_linear_i8<8, true>, 8) : go(k_linear_i8<8, false>, 8);
+}
+
+size_t ffn_i8_workspace(int E, int H, int I, int T, int k) {
+    (void)E;
+    (void)H;
+    return (size_t)T * k * I * 4;  // h
+}
+
+cudaError_t launch_ffn_i8(const FfnI8Args &a, cudaStream_t s) {
+    const int64_t R = (int64_t)a.T * a.k;
+    if (R == 0) return cudaSuccess;
+    float *h = static_cast<float *>(a.ws);
+    const int64_t b1 = R * (a.L.I / kWarps), b2 = R * (a.L.H / kRows2);
+    if (b1 > INT32_MAX || b2 > INT32_MAX) return cudaErrorInvalidValue;
+    const cudaError_t err = launch_pdl(k_ffn_i8_gemv1, dim3((unsigned)b1), dim3(32 * kWarps), 0, s, a, h);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(k_ffn_i8_gemv2, dim3((unsigned)b2), dim3(32 * kWarps), (size_t)a.L.I, s, a, (const float *)h);
+}
+
+cudaError_t i8_take_error(unsigned *code, unsigned *info) {
+    unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_i8_error, sizeof(unsigned));
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(info, g_i8_error_info, sizeof(unsigned));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_i8_error, &zero, sizeof(unsigned));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_i8_error_info, &zero, sizeof(unsigned));
+    return e;
+}
+
+}  // namespace moe

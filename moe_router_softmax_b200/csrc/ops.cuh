@@ -1,0 +1,73 @@
+// ops.cuh -- the operators around int8 experts (scored routing, int8 products,
+// the int8-activation FFN, the block norms): what abi.cu hands to their
+// launchers.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// Scored routing (route_scored.cu).
+struct ScoredArgs {
+    const float *logits, *bias;  // [T][E]; [E] or null
+    int T, E, k;
+    int sigmoid, n_group, group_size, topk_group, group_top, renorm;
+    float scale;
+    int32_t *ids;
+    float *w;
+};
+cudaError_t launch_route_scored(const ScoredArgs &a, cudaStream_t s);
+
+// Block norms (norm.cu).
+struct NormArgs {
+    const float *rows;  // combine source: rows, route_pos, w (k routes per token), or null
+    const int32_t *route_pos;
+    const float *w;
+    int k;
+    const uint16_t *z;         // dense source, or null
+    const uint16_t *residual;  // with a block source; without one the row to normalise
+    const uint16_t *post_w, *next_w;
+    const float *gate_h, *gate_t;
+    float eps, offset, residual_scale, block_scale;
+    int T, H;
+    uint16_t *y, *xn;
+    int8_t *xq;
+    float *sx;
+};
+cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t s);
+
+// int8 x int8 products (i8_gemv.cu).
+struct LinearArgs {
+    const int8_t *xq, *wq;  // [T][K], [N][K]
+    const float *sx, *sw;   // [T], [N]
+    int T, N, K;
+    void *y;                // [T][N] bf16 or fp32
+    int fp32;
+};
+cudaError_t launch_linear_i8(const LinearArgs &a, cudaStream_t s);
+
+// Grouped FFN with int8 activations over int8 experts (i8_gemv.cu).
+struct FfnI8Args {
+    LayerView L;
+    const int8_t *xq;  // [T][H]
+    const float *sx;   // [T]
+    int T, k;
+    const int32_t *counts, *offsets, *sorted_route;
+    float *rows;       // [T k][H], sorted order
+    void *ws;
+};
+size_t ffn_i8_workspace(int E, int H, int I, int T, int k);
+cudaError_t launch_ffn_i8(const FfnI8Args &a, cudaStream_t s);
+cudaError_t i8_take_error(unsigned *code, unsigned *info);
+
+__device__ __forceinline__ float gelu_tanh_f(float v) {
+    const float u = 0.7978845608028654f * (v + 0.044715f * v * v * v);  // sqrt(2/pi)
+    return 0.5f * v * (1.0f + tanhf(u));
+}
+
+// int8 code of v at scale s (moe_quantize_int8's steps); 0 at s = 0 and for a NaN.
+__device__ __forceinline__ int code_i8(float v, float s) {
+    return s != 0.0f ? max(-127, min(127, (int)rintf(__fdiv_rn(v, s)))) : 0;
+}
+
+}  // namespace moe

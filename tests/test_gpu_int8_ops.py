@@ -1,0 +1,531 @@
+"""The operators around int8 experts on the GPU, against their 64-bit references
+(int8_ops_ref): scored routing, int8 products, the int8-activation FFN, the block
+norms, and a decoder layer's run of them, eager and from a CUDA graph."""
+import numpy as np
+import pytest
+import torch
+
+import int8_ops_ref as ref
+import moe_router_softmax_b200 as moe
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def bf16(a):
+    """(device bf16, its value in fp64) of a float array."""
+    t = torch.from_numpy(np.ascontiguousarray(a, np.float32)).bfloat16()
+    return t.to(DEV), t.double().numpy()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def no_device_error():
+    assert moe.moe_take_device_errors() == (0, 0)
+
+
+# ------------------------------------------------------------------ routing
+
+def check_route(lg, k, bias=None, score="softmax", **kw):
+    sc = {"softmax": moe.MOE_SCORE_SOFTMAX, "sigmoid": moe.MOE_SCORE_SIGMOID}[score]
+    ids, w = moe.moe_route_scored(dev(lg), k, bias=None if bias is None else dev(bias), score=sc, **kw)
+    rid, rw = ref.route(lg, k, bias=bias, score=score, **kw)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    # rounded once to fp32 (half a step, or of the smallest subnormal), after fp64 sums whose own error is far below it
+    assert np.all(np.abs(f64(w) - rw) <= (1 + 1e-6) * ref.U32 * np.abs(rw) + 2.0 ** -149)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 128, 8), (3, 33, 5), (5, 64, 32), (2, 200, 7), (17, 256, 8),
+                                   (2, 500, 4), (3, 1000, 32), (2, 1024, 1), (129, 96, 6)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_scored(T, E, k, score):
+    r = np.random.default_rng([T, E, k])
+    lg = (2 * r.standard_normal((T, E))).astype(np.float32)
+    b = (0.1 * r.standard_normal(E)).astype(np.float32)
+    check_route(lg, k, score=score)
+    check_route(lg, k, bias=b, score=score, renorm=False, scale=2.5)
+    check_route(lg, k, bias=10 * b, score=score)  # a bias that outweighs the scores
+
+
+@pytest.mark.parametrize("T,E,G,tg,gt,k", [
+    (1, 256, 8, 4, 2, 8), (9, 256, 8, 4, 1, 8), (3, 160, 8, 3, 2, 6), (4, 165, 5, 3, 1, 6), (2, 66, 22, 3, 2, 6),
+    (2, 1024, 32, 7, 2, 32), (3, 96, 3, 1, 2, 32), (5, 64, 32, 32, 2, 32), (2, 30, 30, 4, 1, 4), (1, 1000, 8, 2, 2, 9),
+    (3, 68, 17, 5, 2, 20), (2, 12, 6, 6, 1, 12)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_scored_groups(T, E, G, tg, gt, k, score):
+    r = np.random.default_rng([T, E, G])
+    lg = (2 * r.standard_normal((T, E))).astype(np.float32)
+    b = (0.1 * r.standard_normal(E)).astype(np.float32)
+    for bias in (None, b):
+        check_route(lg, k, bias=bias, score=score, n_group=G, topk_group=tg, group_top=gt)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("G", [1, 4])
+def test_route_scored_masks_and_ties(score, G):
+    low, E, k = ref.LOWEST, 32, 6
+    r = np.random.default_rng(3)
+    lg = r.standard_normal((12, E)).astype(np.float32)
+    lg[0] = 0.0                                   # all equal
+    lg[1] = -np.inf                               # nothing left
+    lg[2] = np.nan
+    lg[3] = low
+    lg[4, 3:] = -np.inf                           # fewer live than k
+    lg[5, ::2] = np.nan
+    lg[6, 5] = np.inf
+    lg[7, 5] = lg[7, 9] = np.inf                  # two of them
+    lg[8] = np.repeat(lg[8, ::4], 4)              # ties in runs
+    lg[9, 8:16] = low                             # a whole group of four
+    lg[10] = -200.0 - np.arange(E)                # tiny scores
+    lg[11] = np.where(np.arange(E) % 3 == 0, -0.0, 0.0)
+    kw = dict(score=score, n_group=G, topk_group=min(G, 2), group_top=1 + (G > 1))
+    check_route(lg, k, **kw)
+    b = np.zeros(E, np.float32)
+    b[[0, 9, 17]] = [-np.inf, np.nan, low]
+    check_route(lg, k, bias=b, **kw)
+    check_route(lg, k, bias=b, renorm=False, **kw)
+    check_route(lg, k, bias=np.full(E, -np.inf, np.float32), **kw)
+
+
+def test_route_scored_decides_in_64_bits():
+    """Choices nearer to one another than fp32 tells apart."""
+    E = 64
+    lg = np.zeros((2, E), np.float32)
+    b = np.zeros(E, np.float32)
+    lg[:, 40], lg[:, 7] = 1.0, np.nextafter(np.float32(1.0), np.float32(2.0))
+    lg[1, 7] = np.nextafter(np.float32(1.0), np.float32(0.0))
+    for score in ("softmax", "sigmoid"):
+        check_route(lg, 2, bias=b, score=score)
+        check_route(lg, 2, bias=b + np.float32(1000.0), score=score)
+
+
+def test_route_scored_feeds_the_permute():
+    T, E, k = 21, 48, 4
+    r = np.random.default_rng(5)
+    lg = r.standard_normal((T, E)).astype(np.float32)
+    lg[4] = -np.inf
+    lg[6, 2:] = -np.inf
+    ids, w = moe.moe_route_scored(dev(lg), k)
+    counts, offsets, sr, rp = (t.cpu().numpy() for t in moe.moe_permute(ids, E))
+    flat = ids.cpu().numpy().ravel()
+    assert counts.tolist() == [int((flat == e).sum()) for e in range(E)]
+    assert np.array_equal(rp < 0, flat < 0) and (rp[4 * k:5 * k] == -1).all()
+
+
+# ------------------------------------------------------------------ int8 product
+
+def random_codes(r, *shape, full=False):
+    q = r.integers(-128 if full else -127, 128, shape, dtype=np.int64).astype(np.int8)
+    return q
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 8, 9, 16, 31, 64, 65, 130, 257])
+@pytest.mark.parametrize("N,K", [(1, 16), (7, 64), (33, 80), (128, 128), (130, 272), (300, 1040), (64, 2816)])
+def test_linear_int8(T, N, K):
+    r = np.random.default_rng([T, N, K])
+    xq, wq = random_codes(r, T, K, full=True), random_codes(r, N, K, full=True)
+    sx = (0.01 + r.random(T)).astype(np.float32)
+    sw = ((0.01 + r.random(N)) * np.where(r.random(N) < 0.5, -1, 1)).astype(np.float32)
+    y = ref.linear(xq, sx, wq, sw)
+    a = [dev(v) for v in (xq, sx, wq, sw)]
+    out = moe.moe_linear_int8(*a, dtype=torch.float32)
+    # the exact sum: one rounding to fp32 and two products, half a step each
+    assert np.all(np.abs(f64(out) - y) <= 3 * (1 + 1e-6) * ref.U32 * np.abs(y))
+    out = moe.moe_linear_int8(*a)
+    assert np.all(np.abs(f64(out) - y) <= (ref.UBF * (1 + 3 * ref.U32) + 3 * ref.U32) * (1 + 1e-6) * np.abs(y))
+    no_device_error()
+
+
+@pytest.mark.parametrize("T", [1, 4, 40])
+def test_linear_int8_extreme_sums(T):
+    """The largest sums int32 has to hold, and rows of zero codes and scales."""
+    K, N = 65536, 40
+    xq = np.full((T, K), -128, np.int8)
+    wq = np.full((N, K), -128, np.int8)
+    wq[1::2] = 127
+    wq[5] = 0
+    sx, sw = np.ones(T, np.float32), np.ones(N, np.float32)
+    sx[0], sw[3] = 0.0, 0.0
+    y = ref.linear(xq, sx, wq, sw)
+    out = moe.moe_linear_int8(dev(xq), dev(sx), dev(wq), dev(sw), dtype=torch.float32)
+    assert np.all(np.abs(f64(out) - y) <= 3 * (1 + 1e-6) * ref.U32 * np.abs(y))
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_linear_int8_leaves_the_rest(T):
+    """Rows and columns around an output that lies inside a larger buffer."""
+    N, K = 37, 96
+    r = np.random.default_rng(T)
+    a = [dev(v) for v in (random_codes(r, T, K), np.ones(T, np.float32), random_codes(r, N, K), np.ones(N, np.float32))]
+    buf = torch.full(((T * N + 15) // 8 * 8 + 64,), 7.0, device=DEV)
+    y = buf[32:32 + T * N].view(T, N)
+    moe.moe_linear_int8(*a, y=y)
+    assert torch.equal(y, moe.moe_linear_int8(*a, dtype=torch.float32))
+    assert (buf[:32] == 7).all() and (buf[32 + T * N:] == 7).all()
+
+
+# ------------------------------------------------------------------ FFN with int8 activations
+
+def int8_layer(E, H, I, seed, slots=None, missing=()):
+    """Layer with random codes; its pieces on the host.  `slots`: slot table."""
+    r = np.random.default_rng(seed)
+    q13, q2 = random_codes(r, E, 2 * I, H), random_codes(r, E, H, I)
+    s13 = (0.002 * (0.5 + r.random((E, 2 * I)))).astype(np.float32)
+    s2 = (0.002 * (0.5 + r.random((E, H)))).astype(np.float32)
+    eb = (moe.moe_expert_bytes(moe.MOE_W_INT8, H, I) + 255) // 256 * 256
+    blobs = np.zeros((E, eb), np.uint8)
+    for e in range(E):
+        b = np.concatenate([v[e].view(np.uint8).ravel() for v in (q13, s13, q2, s2)])
+        blobs[e, :b.size] = b
+    home = blobs.copy()
+    pool = table = None
+    if slots is not None:
+        pool = np.zeros((max(slots) + 1, eb), np.uint8)
+        for e, s in enumerate(slots):
+            if s >= 0:
+                pool[s] = blobs[e]
+                home[e] = 0xA5
+        pool, table = dev(pool.ravel()), dev(np.array(slots, np.int32))
+    L = moe.MoeLayer(moe.MOE_W_INT8, E, H, I, dev(home.ravel()), pool=pool, slot_table=table, expert_bytes=eb)
+    return L, (q13, s13, q2, s2)
+
+
+def tokens(T, H, seed):
+    r = np.random.default_rng([seed, T, H])
+    q, s = ref.codes(r.standard_normal((T, H)) * np.exp(0.5 * r.standard_normal((T, 1))))
+    return q.astype(np.int8), s.astype(np.float32)
+
+
+def check_ffn(L, pieces, xq, sx, ids, rows, rp, only=None):
+    T, k = ids.shape
+    rows, rp = f64(rows), rp.cpu().numpy()
+    q13, s13, q2, s2 = pieces
+    for t in range(T):
+        if only is not None and t not in only:
+            continue
+        for j in range(k):
+            e, p = ids[t, j], rp[t * k + j]
+            if e < 0 or e >= L.E:
+                assert p == -1
+                continue
+            row, tol = ref.ffn_row(xq[t], sx[t], q13[e], s13[e], q2[e], s2[e])
+            assert np.all(np.abs(rows[p] - row) <= tol), (t, j, float((np.abs(rows[p] - row) - tol).max()))
+
+
+@pytest.mark.parametrize("E,H,I,k", [(8, 256, 128, 2), (5, 64, 64, 1), (16, 320, 192, 4), (12, 128, 704, 3)])
+@pytest.mark.parametrize("T", [1, 2, 3, 7, 20, 65, 150])
+def test_ffn_w8a8(E, H, I, k, T):
+    L, pieces = int8_layer(E, H, I, seed=E + H)
+    xq, sx = tokens(T, H, seed=k)
+    r = np.random.default_rng([T, E])
+    ids = np.argsort(r.standard_normal((T, E)) + 0.7 * r.standard_normal(E), axis=1)[:, :k].astype(np.int32)
+    if T > 2:
+        ids[1, 0] = -1          # a dropped route
+        ids[2, k - 1] = E + 3   # an id that is none
+        xq[0], sx[0] = 0, 0.0   # a token of zeros
+    counts, offsets, sr, rp = moe.moe_permute(dev(ids), E)
+    rows = torch.full((T * k, H), float("nan"), device=DEV)
+    moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(sx), k, counts, offsets, sr, rows=rows)
+    check_ffn(L, pieces, xq, sx, ids, rows, rp)
+    n = int(offsets[-1])
+    assert torch.isnan(rows[n:]).all() and torch.isfinite(rows[:n]).all()  # rows behind the last route: untouched
+    again = moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(sx), k, counts, offsets, sr)
+    assert torch.equal(again[:n], rows[:n])
+    no_device_error()
+
+
+@pytest.mark.parametrize("T", [1, 4, 64, 300])
+def test_ffn_w8a8_repository_shape(T):
+    """128 experts, hidden 2816, intermediate 704, top-8; a few tokens checked in full."""
+    E, H, I, k = 128, 2816, 704, 8
+    L, pieces = int8_layer(E, H, I, seed=1)
+    xq, sx = tokens(T, H, seed=2)
+    ids, w = moe.moe_route_scored(torch.randn((T, E), device=DEV, generator=torch.Generator(DEV).manual_seed(T)), k)
+    counts, offsets, sr, rp = moe.moe_permute(ids, E)
+    rows = moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(sx), k, counts, offsets, sr)
+    check_ffn(L, pieces, xq, sx, ids.cpu().numpy(), rows, rp, only={0, T // 2, T - 1})
+    no_device_error()
+
+
+@pytest.mark.parametrize("T", [1, 3, 80])
+def test_ffn_w8a8_every_token_to_one_expert(T):
+    E, H, I = 6, 192, 128
+    L, pieces = int8_layer(E, H, I, seed=9)
+    xq, sx = tokens(T, H, seed=3)
+    ids = np.full((T, 1), 4, np.int32)
+    counts, offsets, sr, rp = moe.moe_permute(dev(ids), E)
+    rows = moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(sx), 1, counts, offsets, sr)
+    check_ffn(L, pieces, xq, sx, ids, rows, rp)
+    # no route at all
+    counts, offsets, sr, rp = moe.moe_permute(dev(np.full((T, 1), -1, np.int32)), E)
+    rows.fill_(3.0)
+    moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(sx), 1, counts, offsets, sr, rows=rows)
+    assert (rows == 3.0).all()
+    no_device_error()
+
+
+@pytest.mark.parametrize("T", [1, 5, 70])
+def test_ffn_w8a8_slot_table(T):
+    E, H, I, k = 8, 256, 128, 3
+    slots = [-1, 11, 0, -1, 5, 7, -1, 2]
+    L, pieces = int8_layer(E, H, I, seed=4, slots=slots)
+    xq, sx = tokens(T, H, seed=6)
+    r = np.random.default_rng(T)
+    ids = np.argsort(r.random((T, E)), axis=1)[:, :k].astype(np.int32)
+    counts, offsets, sr, rp = moe.moe_permute(dev(ids), E)
+    rows = moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(sx), k, counts, offsets, sr)
+    check_ffn(L, pieces, xq, sx, ids, rows, rp)
+    no_device_error()
+    # a slot past the pool: refused, reported, the other rows as before
+    L.slot_table[4] = L.pool_slots
+    out = torch.full_like(rows, float("nan"))
+    moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(sx), k, counts, offsets, sr, rows=out)
+    bad = np.zeros(T * k, bool)
+    bad[rp.cpu().numpy()[ids.ravel() == 4]] = True
+    bad = torch.from_numpy(bad).to(DEV)
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], rows[~bad])
+    code, info = moe.moe_take_device_errors()
+    assert (code != 0 and info == L.pool_slots) if bool(bad.any()) else code == 0
+
+
+def test_ffn_w8a8_empty_batch():
+    L, _ = int8_layer(4, 64, 64, seed=0)
+    z = lambda *s, d=torch.int32: torch.zeros(s, dtype=d, device=DEV)  # noqa: E731
+    rows = moe.moe_grouped_ffn_w8a8(L, z(0, 64, d=torch.int8), z(0, d=torch.float32), 2, z(4), z(5), z(0))
+    assert rows.shape == (0, 64)
+
+
+# ------------------------------------------------------------------ norms
+
+def check_next(out, y_stored, nw, eps, off):
+    n, rel = ref.norm(y_stored, nw, eps, off)
+    if out.xn is not None:
+        assert np.all(np.abs(f64(out.xn) - n) <= (ref.UBF * (1 + rel) + rel) * np.abs(n) + 2.0 ** -134)
+    if out.xq is not None:
+        _, s = ref.codes(n)
+        assert np.all(np.abs(f64(out.sx) - s) <= (rel + 2 * ref.U32) * s + 2.0 ** -149)
+        q = n / np.where(s > 0, s, 1.0)[:, None]
+        # the nearest code of a quotient that is off by both errors
+        assert np.all(np.abs(f64(out.xq) - q) <= 0.5 + 127 * (2 * rel + 3 * ref.U32))
+
+
+@pytest.mark.parametrize("T,H", [(1, 64), (3, 128), (2, 320), (5, 2816), (1, 4160), (2, 8192), (1, 8256), (2, 16384),
+                                 (300, 192), (33, 1024)])
+@pytest.mark.parametrize("offset", [0.0, 1.0])
+def test_norm(T, H, offset):
+    r = np.random.default_rng([T, H])
+    x = r.standard_normal((T, H)) * np.exp(r.standard_normal((T, 1)))
+    x[:, 3] *= 30
+    if T > 1:
+        x[1] = 0.0
+    xt, xv = bf16(x)
+    wt, wv = bf16(1.0 + 0.3 * r.standard_normal(H))
+    out = moe.moe_norm(xt, wt, eps=1e-5, offset=offset, codes=True)
+    check_next(out, xv, wv, 1e-5, offset)
+    only = moe.moe_norm(xt, wt, eps=1e-5, offset=offset, codes=True, want_xn=False)
+    assert only.xn is None and torch.equal(only.xq, out.xq) and torch.equal(only.sx, out.sx)
+    assert torch.equal(moe.moe_norm(xt, wt, eps=1e-5, offset=offset).xn, out.xn)
+    if T > 1:
+        assert float(out.sx[1]) == 0.0 and (out.xq[1] == 0).all()
+
+
+@pytest.mark.parametrize("T,H", [(1, 64), (3, 192), (4, 2816), (1, 8256), (2, 16384), (70, 256)])
+@pytest.mark.parametrize("form", ["plain", "norm", "gates", "all"])
+@pytest.mark.parametrize("k", [0, 1, 8, 11, 32])
+def test_after_block(T, H, form, k):
+    r = np.random.default_rng([T, H, k])
+    eps, off, rs, bs = 1e-6, 0.5, 0.75, -1.25
+    res, resv = bf16(r.standard_normal((T, H)))
+    pw = gh = gt = nw = None
+    pv = ghv = gtv = nv = None
+    if form in ("norm", "all"):
+        pw, pv = bf16(0.3 * r.standard_normal(H))
+    if form in ("gates", "all"):
+        ghv, gtv = r.standard_normal(H).astype(np.float32), r.standard_normal(T).astype(np.float32)
+        gh, gt = dev(ghv), dev(gtv)
+    if form in ("norm", "all"):
+        nw, nv = bf16(0.3 * r.standard_normal(H))
+    kw = dict(post_weight=pw, gate_h=gh, gate_t=gt, next_weight=nw, eps=eps, offset=off, residual_scale=rs,
+              block_scale=bs, codes=nw is not None)
+    if k == 0:
+        z, zv = bf16(r.standard_normal((T, H)))
+        mag = np.zeros_like(zv)
+        out = moe.moe_residual_norm(z, res, **kw)
+    else:
+        rows = r.standard_normal((T * k, H)).astype(np.float32)
+        pos = r.permutation(T * k).astype(np.int32)
+        w = r.random((T, k)).astype(np.float32)
+        pos[r.random(T * k) < 0.1] = -1
+        if T > 2:
+            pos[k:2 * k] = -1            # a token without a route
+            pos[2 * k] = T * k + 5       # and a position that is none
+        zv, mag = ref.combine(rows, pos, w)
+        out = moe.moe_combine_norm(dev(rows), dev(pos), dev(w), res, **kw)
+    y, tol = ref.after_block(zv, mag, resv, pv, ghv, gtv, eps, off, rs, bs)
+    assert np.all(np.abs(f64(out.y) - y) <= ref.UBF * (np.abs(y) + tol) + tol + 2.0 ** -134)
+    if nw is None:
+        assert out.xn is None and out.xq is None and out.sx is None
+        return
+    check_next(out, f64(out.y), nv, eps, off)
+    # the same as the two calls, and in place
+    two = moe.moe_norm(out.y, nw, eps=eps, offset=off, codes=True)
+    assert torch.equal(two.xn, out.xn) and torch.equal(two.xq, out.xq) and torch.equal(two.sx, out.sx)
+    if k == 0:
+        for tgt in ("residual", "z"):
+            a, b = z.clone(), res.clone()
+            o = moe.moe_residual_norm(a, b, y=b if tgt == "residual" else a, **kw)
+            assert torch.equal(o.y, out.y) and torch.equal(o.xn, out.xn)
+    else:
+        b = res.clone()
+        o = moe.moe_combine_norm(dev(rows), dev(pos), dev(w), b, y=b, **kw)
+        assert torch.equal(o.y, out.y) and torch.equal(o.xq, out.xq)
+
+
+def test_norm_with_infinities_and_nan():
+    x = torch.ones((4, 128), dtype=torch.bfloat16, device=DEV)
+    x[1, 7] = float("nan")
+    x[2, 7] = float("inf")
+    w = torch.ones(128, dtype=torch.bfloat16, device=DEV)
+    out = moe.moe_norm(x, w, codes=True)
+    clean = moe.moe_norm(torch.ones((1, 128), dtype=torch.bfloat16, device=DEV), w, codes=True)
+    assert torch.isnan(out.xn[1]).all() and (out.xq[1] == 0).all()
+    assert torch.isnan(out.xn[2, 7]) and (out.xn[2, :7] == 0).all()
+    for t in (0, 3):  # the rows beside them
+        assert torch.equal(out.xn[t], clean.xn[0]) and torch.equal(out.xq[t], clean.xq[0])
+
+
+def test_empty_batches():
+    e = lambda *s, d=torch.float32: torch.empty(s, dtype=d, device=DEV)  # noqa: E731
+    w = torch.ones(64, dtype=torch.bfloat16, device=DEV)
+    x = e(0, 64, d=torch.bfloat16)
+    out = moe.moe_norm(x, w, codes=True)
+    assert out.xn.shape == out.xq.shape == (0, 64) and out.sx.shape == (0,)
+    assert moe.moe_residual_norm(x, x, w, next_weight=w, codes=True).y.shape == (0, 64)
+    assert moe.moe_combine_norm(e(0, 64), e(0, d=torch.int32), e(0, 3), x, w, next_weight=w).y.shape == (0, 64)
+    assert moe.moe_linear_int8(out.xq, out.sx, torch.ones((8, 64), dtype=torch.int8, device=DEV), e(8)).shape == (0, 8)
+    assert moe.moe_route_scored(e(0, 16), 2)[0].shape == (0, 2)
+
+
+# ------------------------------------------------------------------ refusals of the binding
+
+def test_binding_refusals():
+    i8 = torch.zeros((4, 64), dtype=torch.int8, device=DEV)
+    s = torch.ones(4, device=DEV)
+    with pytest.raises(ValueError, match="shape"):
+        moe.moe_linear_int8(i8, s[:3], i8, s)
+    with pytest.raises(ValueError, match="shape"):
+        moe.moe_linear_int8(i8, s, i8[:, :32].contiguous(), s)
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.moe_linear_int8(torch.zeros((64, 4), dtype=torch.int8, device=DEV).t(), s, i8, s)
+    with pytest.raises(ValueError, match="dtype"):
+        moe.moe_linear_int8(i8, s, i8, s, dtype=torch.float16)
+    with pytest.raises(ValueError, match="expected"):
+        moe.moe_linear_int8(i8, s.cpu(), i8, s)
+    with pytest.raises(moe.MoeError):
+        moe.moe_linear_int8(i8.flatten()[8:8 + 64].view(1, 64), s[:1], i8, s)  # 8-byte aligned
+    with pytest.raises(ValueError, match="shape"):
+        moe.moe_route_scored(torch.zeros((2, 8), device=DEV), 2, bias=torch.zeros(7, device=DEV))
+    with pytest.raises(ValueError, match="dtype"):
+        moe.moe_route_scored(torch.zeros((2, 8), device=DEV, dtype=torch.bfloat16), 2)
+    with pytest.raises(moe.MoeError, match="k=9"):
+        moe.moe_route_scored(torch.zeros((2, 8), device=DEV), 9)
+    x = torch.zeros((2, 64), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="dtype"):
+        moe.moe_norm(x, x[0].float())
+    with pytest.raises(ValueError, match="shape"):
+        moe.moe_residual_norm(x[:1], x)
+    with pytest.raises(moe.MoeError, match="eps"):
+        moe.moe_norm(x, x[0], eps=0.0)
+
+
+# ------------------------------------------------------------------ a run of them together
+
+def _decoder(T, E=16, H=256, I=128, k=4, n=3):
+    """A chain of n MoE blocks over one residual stream; returns the call and what it writes."""
+    g = torch.Generator(DEV).manual_seed(T)
+    layers = [int8_layer(E, H, I, seed=20 + l)[0] for l in range(n)]
+    rnd = lambda *s: torch.randn(s, device=DEV, generator=g)  # noqa: E731
+    pre = [(1 + 0.1 * rnd(H)).bfloat16() for _ in range(n + 1)]
+    post = [(1 + 0.1 * rnd(H)).bfloat16() for _ in range(n)]
+    qr, sr_ = moe.moe_quantize_int8((0.1 * rnd(E, H)).bfloat16())
+    bias = 0.02 * rnd(E)
+    x0 = rnd(T, H).bfloat16()
+    ws = [torch.empty(moe.moe_grouped_ffn_w8a8_workspace(layers[0], T, k), dtype=torch.uint8, device=DEV) for _ in range(n)]
+
+    def run():
+        h = moe.moe_norm(x0, pre[0], codes=True)
+        x, got = x0, []
+        for l in range(n):
+            lg = moe.moe_linear_int8(h.xq, h.sx, qr, sr_, dtype=torch.float32)
+            ids, w = moe.moe_route_scored(lg, k, bias=bias, score=moe.MOE_SCORE_SIGMOID, n_group=4, topk_group=2,
+                                          group_top=2, scale=1.5)
+            counts, offsets, srt, rp = moe.moe_permute(ids, E)
+            rows = moe.moe_grouped_ffn_w8a8(layers[l], h.xq, h.sx, k, counts, offsets, srt, ws=ws[l])
+            h = moe.moe_combine_norm(rows, rp, w, x, post[l], next_weight=pre[l + 1], codes=True)
+            x = h.y
+            got += [ids, w, h.y, h.xn, h.xq, h.sx]
+        return got
+
+    return run
+
+
+@pytest.mark.parametrize("T", [1, 3, 40, 130])
+def test_run_together_replayed_and_on_other_streams(T):
+    run = _decoder(T)
+    eager = [t.clone() for t in run()]
+    assert all(torch.isfinite(t.float()).all() for t in eager)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    for _ in range(3):
+        for t in out:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, eager))
+    # two streams at once, each with its own buffers
+    other = _decoder(T)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s1):
+        a = run()
+    with torch.cuda.stream(s2):
+        b = other()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(a, eager)) and all(torch.equal(p, q) for p, q in zip(b, eager))
+    no_device_error()
+
+
+def test_run_together_against_the_formulas():
+    """One block, each step held to its reference on the step's own inputs."""
+    T, E, H, I, k = 9, 16, 256, 128, 4
+    L, pieces = int8_layer(E, H, I, seed=30)
+    r = np.random.default_rng(8)
+    xt, xv = bf16(r.standard_normal((T, H)))
+    nw, nv = bf16(1 + 0.1 * r.standard_normal(H))
+    h = moe.moe_norm(xt, nw, codes=True)
+    check_next(h, xv, nv, 1e-6, 0.0)
+    wr = dev((0.1 * r.standard_normal((E, H))).astype(np.float32)).bfloat16()
+    qr, sr_ = moe.moe_quantize_int8(wr)
+    lg = moe.moe_linear_int8(h.xq, h.sx, qr, sr_, dtype=torch.float32)
+    ids, w = moe.moe_route_scored(lg, k)
+    rid, rw = ref.route(lg.cpu().numpy(), k)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    counts, offsets, srt, rp = moe.moe_permute(ids, E)
+    rows = moe.moe_grouped_ffn_w8a8(L, h.xq, h.sx, k, counts, offsets, srt)
+    check_ffn(L, pieces, h.xq.cpu().numpy(), h.sx.cpu().numpy(), rid, rows, rp)
+    out = moe.moe_combine_norm(rows, rp, w, xt, nw, next_weight=nw, codes=True)
+    z, mag = ref.combine(rows.cpu().numpy(), rp.cpu().numpy(), w.cpu().numpy())
+    y, tol = ref.after_block(z, mag, xv, nv, None, None, 1e-6, 0.0, 1.0, 1.0)
+    assert np.all(np.abs(f64(out.y) - y) <= ref.UBF * (np.abs(y) + tol) + tol)
+    check_next(out, f64(out.y), nv, 1e-6, 0.0)
+    # without its norms and residual the block's end is moe_combine, bit for bit
+    plain = moe.moe_combine_norm(rows, rp, w, torch.zeros_like(xt))
+    assert torch.equal(plain.y, moe.moe_combine(rows, rp, w))
