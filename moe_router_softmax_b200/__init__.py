@@ -554,11 +554,13 @@ def _device_of(t: torch.Tensor, ndim: int, name: str):
 def _call(fn, dev, stream, *args) -> None:
     """Run an entry point on `dev`, on `stream` or the device's current stream."""
     idx = dev.index
+    # the stream's raw handle: building a Stream object would cost a third of a small call
+    raw = torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream
     if idx == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(idx):
-            st = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
+            st = fn(*args, raw)
     if st != MOE_OK:
         _check(st)
 
@@ -571,8 +573,8 @@ def moe_route_scored(logits: torch.Tensor, k: int, bias: torch.Tensor | None = N
     int32 [T, k] (-1 where a token has fewer than k live experts) and fp32 [T, k]."""
     dev = _device_of(logits, 2, "logits")
     T, E = logits.shape
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev) if ids is None else ids
-    w = torch.empty((T, k), dtype=torch.float32, device=dev) if w is None else w
+    ids = logits.new_empty((T, k), dtype=torch.int32) if ids is None else ids
+    w = logits.new_empty((T, k), dtype=torch.float32) if w is None else w
     _call(_lib.moe_route_scored, dev, stream, _arg(logits, (T, E), torch.float32, "logits", dev),
           _arg(bias, (E,), torch.float32, "bias", dev), T, E, k, score, n_group, topk_group, group_top, bool(renorm),
           scale, _arg(ids, (T, k), torch.int32, "ids", dev), _arg(w, (T, k), torch.float32, "w", dev))
@@ -587,7 +589,7 @@ def moe_linear_int8(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: to
     T, K = xq.shape
     N = wq.shape[0]
     if y is None:
-        y = torch.empty((T, N), dtype=dtype, device=dev)
+        y = xq.new_empty((T, N), dtype=dtype)
     _call(_lib.moe_linear_int8, dev, stream, _arg(xq, (T, K), torch.int8, "xq", dev),
           _arg(sx, (T,), torch.float32, "sx", dev), _arg(wq, (N, K), torch.int8, "wq", dev),
           _arg(sw, (N,), torch.float32, "sw", dev), T, N, K,
@@ -629,12 +631,12 @@ class NormOut(NamedTuple):
     sx: Optional[torch.Tensor]  # fp32 [T], their scales
 
 
-def _norm_out(T, H, dev, y, xn, xq, sx, want_xn, codes) -> NormOut:
+def _norm_out(like, T, H, y, xn, xq, sx, want_xn, codes) -> NormOut:
     if xn is None and want_xn:
-        xn = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        xn = like.new_empty((T, H), dtype=torch.bfloat16)
     if codes:
-        xq = torch.empty((T, H), dtype=torch.int8, device=dev) if xq is None else xq
-        sx = torch.empty((T,), dtype=torch.float32, device=dev) if sx is None else sx
+        xq = like.new_empty((T, H), dtype=torch.int8) if xq is None else xq
+        sx = like.new_empty((T,), dtype=torch.float32) if sx is None else sx
     return NormOut(y, xn, xq, sx)
 
 
@@ -645,7 +647,7 @@ def moe_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: f
     (``want_xn``) and, with ``codes``, as int8 codes with a scale per token."""
     dev = _device_of(x, 2, "x")
     T, H = x.shape
-    o = _norm_out(T, H, dev, None, xn, xq, sx, want_xn, codes)
+    o = _norm_out(x, T, H, None, xn, xq, sx, want_xn, codes)
     bf = torch.bfloat16
     _call(_lib.moe_norm, dev, stream, _arg(x, (T, H), bf, "x", dev), _arg(weight, (H,), bf, "weight", dev), T, H, eps,
           offset, _arg(o.xn, (T, H), bf, "xn", dev), _arg(o.xq, (T, H), torch.int8, "xq", dev),
@@ -658,9 +660,9 @@ def _after_block(fn, src, residual, post_weight, gate_h, gate_t, next_weight, ep
     dev = _device_of(residual, 2, "residual")
     T, H = residual.shape
     bf, fp = torch.bfloat16, torch.float32
-    y = torch.empty((T, H), dtype=bf, device=dev) if y is None else y
+    y = residual.new_empty((T, H), dtype=bf) if y is None else y
     has_next = next_weight is not None
-    o = _norm_out(T, H, dev, y, xn, xq, sx, want_xn and has_next, codes)
+    o = _norm_out(residual, T, H, y, xn, xq, sx, want_xn and has_next, codes)
     _call(fn, dev, stream, *src(T, H, dev), _arg(residual, (T, H), bf, "residual", dev),
           _arg(post_weight, (H,), bf, "post_weight", dev), _arg(gate_h, (H,), fp, "gate_h", dev),
           _arg(gate_t, (T,), fp, "gate_t", dev), _arg(next_weight, (H,), bf, "next_weight", dev), T, H, eps, offset,

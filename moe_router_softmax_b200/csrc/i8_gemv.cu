@@ -15,6 +15,8 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 4;
+constexpr int kGemvTokens = 8;   // linear: these kernels up to here, then the tensor cores
+constexpr int kGemvRoutes = 32;  // ffn, in routes
 
 // First problem a kernel of this file recorded (0 = none), read and cleared by
 // moe_take_device_errors(): 0x2005 a slot past the pool, 0x2007 a route out of range.
@@ -62,7 +64,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_linear_i8(const LinearArgs a) {
     for (int t = 0; t < TB; ++t) {
         const int sum = __reduce_add_sync(kAll, acc[t]);
         if (lane != t || t0 + t >= a.T) continue;
-        const float v = (float)sum * __ldg(a.sx + t0 + t) * sw;
+        const float v = scaled(sum, __ldg(a.sx + t0 + t), sw);
         const size_t at = (size_t)(t0 + t) * a.N + n;
         if (FP32) static_cast<float *>(a.y)[at] = v;
         else static_cast<uint16_t *>(a.y)[at] = f32_to_bf16_rne(v);
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_ffn_i8_gemv1(const FfnI8Args a,
     if (lane == 0) {
         const float *s13 = reinterpret_cast<const float *>(blob + a.L.off.s13);
         const float sx = __ldg(a.sx + t);
-        h[(size_t)s * I + i] = gelu_tanh_f((float)ag * sx * __ldg(s13 + i)) * ((float)au * sx * __ldg(s13 + I + i));
+        h[(size_t)s * I + i] = gate_up(ag, au, sx, __ldg(s13 + i), __ldg(s13 + I + i));
     }
 }
 
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_ffn_i8_gemv2(const FfnI8Args a,
         for (int c = lane; c < I / 16; c += 32)
             acc = dot16(ld_stream_v4(w + c), reinterpret_cast<const uint4 *>(s_hq)[c], acc);
         acc = __reduce_add_sync(kAll, acc);
-        if (lane == 0) a.rows[(size_t)s * H + n] = (float)acc * sh * __ldg(s2 + n);
+        if (lane == 0) a.rows[(size_t)s * H + n] = scaled(acc, sh, __ldg(s2 + n));
     }
 }
 
@@ -159,6 +161,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_ffn_i8_gemv2(const FfnI8Args a,
 
 cudaError_t launch_linear_i8(const LinearArgs &a, cudaStream_t s) {
     if (a.T == 0) return cudaSuccess;
+    if (a.T > kGemvTokens) return launch_linear_i8_tc(a, s);
     const dim3 block(32 * kWarps);
     auto go = [&](auto kern, int tb) {
         return launch_pdl(kern, dim3((unsigned)((a.N + kWarps - 1) / kWarps), (unsigned)((a.T + tb - 1) / tb)), block, 0,
@@ -168,15 +171,14 @@ cudaError_t launch_linear_i8(const LinearArgs &a, cudaStream_t s) {
     return a.fp32 ? go(k_linear_i8<8, true>, 8) : go(k_linear_i8<8, false>, 8);
 }
 
-size_t ffn_i8_workspace(int E, int H, int I, int T, int k) {
-    (void)E;
-    (void)H;
-    return (size_t)T * k * I * 4;  // h
+size_t ffn_i8_workspace(int H, int I, int T, int k) {
+    return (int64_t)T * k <= kGemvRoutes ? (size_t)T * k * I * 4 : ffn_i8_tc_workspace(H, I, T, k);
 }
 
 cudaError_t launch_ffn_i8(const FfnI8Args &a, cudaStream_t s) {
     const int64_t R = (int64_t)a.T * a.k;
     if (R == 0) return cudaSuccess;
+    if (R > kGemvRoutes) return launch_ffn_i8_tc(a, s);
     float *h = static_cast<float *>(a.ws);
     const int64_t b1 = R * (a.L.I / kWarps), b2 = R * (a.L.H / kRows2);
     if (b1 > INT32_MAX || b2 > INT32_MAX) return cudaErrorInvalidValue;

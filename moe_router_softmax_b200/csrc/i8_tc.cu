@@ -1,0 +1,589 @@
+// i8_tc.cu -- int8 x int8 products on the 5th-generation tensor cores
+// (tcgen05.mma kind::i8: int8 codes from shared memory, int32 sums in TMEM).
+//
+// The same two products as i8_gemv.cu for more than a few tokens: the dense
+// product (moe_linear_int8) and the two grouped products of the FFN with int8
+// activations.  Both operands are codes, so TMA puts them into shared memory in
+// the 128-byte-swizzled K-major layout that the MMA reads and nothing touches
+// them on the way; scales are applied to the sums.
+//
+// The weight rows are the M = 128 operand, the tokens (an expert's routes) N, up
+// to 256 per block:
+//   linear   D[128 x N] = Wq[m0..m0+127] . Xq^T        y[t][m] = D sx[t] sw[m]
+//   phase 1  D rows: 16 gate rows of W13, their 16 up rows, the next 16 gate rows,
+//            ...: a gate row and its up row are 16 lanes apart in one TMEM
+//            quadrant, so an epilogue warp pairs them with one shuffle per two columns
+//            (one half of the lanes finishes the even column, the other the odd one)
+//            h[s][i] = gelu_tanh(g) * u  (fp32)
+//   phase 2  as linear, per expert, over the codes of h; rows[s][m] = D sh[s] s2[m]
+//
+// Persistent CTAs, one per SM; warp 0 TMA producer of the weights, warp 1 TMEM
+// allocation and the MMA issuer, warps 2..5 epilogue (TMEM -> registers ->
+// global; warp w reads lanes 32 (w % 4) ..), warp 6 TMA producer of the tokens.
+// One ring of stages of 128 codes of K (a stage: 128 weight rows and one block of
+// token rows), its depth set by the launch's largest block; two accumulators of 256
+// columns, so that an item's epilogue overlaps the next item's products.  Every
+// wait is bounded: on a timeout the kernel records it and every role drains out.
+#include <algorithm>
+
+#include "ops.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace tc;
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kM = 128;                        // weight rows per tile
+constexpr int kKB = 128;                       // codes of K per stage: one swizzle row
+constexpr int kNMax = 256;                     // tokens per block
+constexpr uint32_t kABytes = kM * kKB;         // 16 KB
+constexpr int kRing = 205 * 1024;
+constexpr int kMaxStages = 12;
+constexpr int kEpiWarps = 4;
+constexpr int kWarpB = 2 + kEpiWarps;
+constexpr int kThreads = 32 * (kWarpB + 1);
+constexpr int kTmemCols = 512;
+
+enum { kLinear = 0, kPhase1 = 1, kPhase2 = 2 };
+
+// First problem a kernel of this file recorded (0 = none), read and cleared by
+// moe_take_device_errors(): 0x1000 | warp for a wait that gave up, 0x2006 a slot
+// past the pool, 0x2008 a route block out of range, 0x2009 a route out of range.
+__device__ unsigned int g_i8tc_error;
+__device__ unsigned int g_i8tc_error_info;
+__device__ __forceinline__ void record_error(unsigned code, unsigned info) {
+    if (atomicCAS(&g_i8tc_error, 0u, code) == 0u) g_i8tc_error_info = info;
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    return mbar_wait_bounded(bar, parity, abort_flag, [=] {
+        record_error(0x1000u | (threadIdx.x >> 5), (unsigned)((smem_u32(bar) << 1) | (parity & 1)));
+    });
+}
+
+struct TcI8Params {
+    LayerView L;                     // phases
+    const int32_t *counts, *offsets; // phases
+    int E;                           // 1 for linear
+    int R;                           // token rows
+    int K, M;                        // length of the products; output rows: N, I (phase 1) or H
+    const float *brow;               // scale per token row
+    const float *wscale;             // linear: scale per output row
+    void *out;                       // y, h or rows
+    int fp32;                        // linear: y in fp32
+};
+
+__device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// {x, row, 16-row block, gate or up, blob} box of W13.
+__device__ __forceinline__ void tma_load_5d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int x, int b, int z,
+                                            uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %4, %6}], [%2], %7;"
+        ::"r"(smem_u32(smem_dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(0), "r"(b), "r"(z), "l"(pol)
+        : "memory");
+}
+
+struct Items {
+    int n_act, total, m_tiles, b_rows, stages;
+};
+
+// Blocks of an expert's n routes: as few as kNMax allows, of even size, a
+// multiple of 16 (the MMA's N).
+__device__ __forceinline__ int blocks_of(int n) { return (n + kNMax - 1) / kNMax; }
+__device__ __forceinline__ int block_rows(int n) {
+    const int nb = blocks_of(n);
+    return ((n + nb - 1) / nb + 15) & ~15;
+}
+
+struct ItemInfo {
+    int e, row0, n, n_mma, mt;
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CUtensorMap map_pool,
+        const __grid_constant__ CUtensorMap map_b16, const __grid_constant__ CUtensorMap map_b32, const TcI8Params p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ int s_base[kMaxE + 1];     // first item of each active expert
+    __shared__ int s_row0[kMaxE];
+    __shared__ int s_cnt[kMaxE];
+    __shared__ uint16_t s_act[kMaxE];
+    __shared__ Items s_items;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int m_tiles = MODE == kPhase1 ? p.M / 64 : (p.M + kM - 1) / kM;
+    const int nk = (p.K + kKB - 1) / kKB;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(&full[i], 2);   // both producers
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], kEpiWarps);
+        }
+        s_abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // dense: one expert that holds every token.  phases: the experts with routes
+    if (MODE != kLinear) {
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) s_cnt[e] = __ldg(p.counts + e);
+        __syncthreads();
+    }
+    if (warp == 0) {
+        int n_act = 0, run = 0, rows = 16;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int n = e < p.E ? (MODE == kLinear ? p.R : s_cnt[e]) : 0;
+            const int off = MODE == kLinear || e >= p.E ? 0 : __ldg(p.offsets + e);
+            __syncwarp();  // every lane has read its count before any is written in place
+            const bool act = n > 0;
+            const unsigned m = __ballot_sync(kAll, act);
+            const int items = act ? m_tiles * blocks_of(n) : 0;
+            if (act) rows = max(rows, block_rows(n));
+            int inc = items;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(kAll, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (act) {
+                const int pos = n_act + __popc(m & ((1u << lane) - 1u));
+                s_act[pos] = (uint16_t)e;
+                s_cnt[pos] = n;
+                s_row0[pos] = off;
+                s_base[pos] = run + inc - items;
+            }
+            run += __shfl_sync(kAll, inc, 31);
+            n_act += __popc(m);
+        }
+        rows = (int)__reduce_max_sync(kAll, (unsigned)rows);
+        if (lane == 0) {
+            // blocks over 32 rows are loaded in boxes of 32
+            const int b_rows = rows <= 32 ? rows : (rows + 31) & ~31;
+            s_base[n_act] = run;
+            s_items = Items{n_act, run, m_tiles, b_rows, min(kMaxStages, kRing / ((int)kABytes + b_rows * kKB))};
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // the next launch may take over SMs as this grid's CTAs finish
+    pdl_launch_dependents();
+    const uint32_t tmem = s_tmem;
+    const int total = s_items.total, n_act = s_items.n_act, S = s_items.stages;
+    const uint32_t stage_bytes = kABytes + (uint32_t)s_items.b_rows * kKB;
+
+    auto decode = [&](int item) {
+        int lo = 0, hi = n_act - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_base[mid] <= item) lo = mid; else hi = mid - 1;
+        }
+        const int rem = item - s_base[lo], nb = rem / m_tiles, n_e = s_cnt[lo], blk = block_rows(n_e);
+        ItemInfo r;
+        r.e = s_act[lo];
+        r.mt = rem - nb * m_tiles;
+        r.row0 = s_row0[lo] + nb * blk;
+        r.n = min(blk, n_e - nb * blk);
+        r.n_mma = (max(r.n, 1) + 15) & ~15;
+        if (MODE != kLinear) {
+            bool bad;
+            expert_slot(p.L, r.e, &bad);
+            if (bad) record_error(0x2006u, (unsigned)__ldg(p.L.slot_table + r.e));
+            if (r.row0 < 0 || r.n < 0 || r.row0 > p.R - r.n) {
+                record_error(0x2008u, (unsigned)item);
+                bad = true;
+            }
+            if (bad) {  // nothing is written for it; its weights are read from home
+                r.n = 0;
+                r.n_mma = 16;
+                r.row0 = 0;
+            }
+        }
+        return r;
+    };
+
+    if (warp == 0) {
+        // -------------------------------------------------- weights
+        if (lane == 0) {
+            // The dense product's weights may come from the launch before; the
+            // phases' launches follow this library's own (gather, codes of h),
+            // which have waited for all before them and write no weights.
+            if (MODE == kLinear) pdl_wait();
+            const uint64_t pol = MODE == kLinear ? l2_policy_last() : l2_policy_first();
+            int st = 0;
+            uint32_t ph = 0;
+            for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
+                const ItemInfo it = decode(item);
+                const CUtensorMap *ma = &map_home;
+                int z = 0;
+                if (MODE != kLinear) {
+                    bool bad;
+                    const int s = expert_slot(p.L, it.e, &bad);
+                    if (s >= 0) ma = &map_pool;
+                    z = s >= 0 ? s : it.e;
+                }
+                bool ok = true;
+                for (int kk = 0; kk < nk; ++kk) {
+                    if (!mbar_wait(&empty[st], ph ^ 1, &s_abort)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&full[st], kABytes);
+                    uint8_t *dst = ring + st * stage_bytes;
+                    if (MODE == kPhase1) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            tma_load_5d(dst + b * (kABytes / 4), ma, &full[st], kk * kKB, it.mt * 4 + b, z, pol);
+                    } else {
+                        tma_load_3d(dst, ma, &full[st], kk * kKB, it.mt * kM, z, pol);
+                    }
+                    if (++st == S) { st = 0; ph ^= 1; }
+                }
+                if (!ok) break;
+            }
+        }
+    } else if (warp == kWarpB) {
+        // -------------------------------------------------- tokens
+        if (lane == 0) {
+            pdl_wait();
+            const uint64_t pol = l2_policy_last();
+            int st = 0;
+            uint32_t ph = 0;
+            for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
+                const ItemInfo it = decode(item);
+                const int box = it.n_mma > 32 ? 32 : 16;
+                const int rows = (it.n_mma + box - 1) & ~(box - 1);  // rows past the block are read, not used
+                bool ok = true;
+                for (int kk = 0; kk < nk; ++kk) {
+                    if (!mbar_wait(&empty[st], ph ^ 1, &s_abort)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&full[st], (uint32_t)rows * kKB);
+                    uint8_t *dst = ring + st * stage_bytes + kABytes;
+                    for (int j = 0; j < rows; j += box)
+                        tma_load_2d(dst + j * kKB, box == 32 ? &map_b32 : &map_b16, &full[st], kk * kKB, it.row0 + j,
+                                    pol);
+                    if (++st == S) { st = 0; ph ^= 1; }
+                }
+                if (!ok) break;
+            }
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            int st = 0, acc = 0;
+            uint32_t ph = 0, aph = 0;
+            for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
+                const ItemInfo it = decode(item);
+                if (!mbar_wait(&tempty[acc], aph ^ 1, &s_abort)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * kNMax);
+                // int32 sums, both operands signed 8-bit, N and M of the tile
+                const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(it.n_mma >> 3) << 17) |
+                                       ((uint32_t)(kM >> 4) << 24);
+                bool ok = true;
+                for (int kk = 0; kk < nk; ++kk) {
+                    if (!mbar_wait(&full[st], ph, &s_abort)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(ring + st * stage_bytes);
+                    const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + kABytes);
+                    // 32 codes of K per MMA: 32 bytes, 2 in the descriptor's address field;
+                    // past K both operands hold zeros
+                    const int steps = min(kKB / 32, (p.K - kk * kKB + 31) / 32);
+                    for (int j = 0; j < steps; ++j)
+                        tc_mma_i8(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (kk | j) != 0);
+                    tc_commit(&empty[st]);
+                    if (++st == S) { st = 0; ph ^= 1; }
+                }
+                if (!ok) break;
+                tc_commit(&tfull[acc]);
+                acc ^= 1;
+                aph ^= acc == 0;
+            }
+        }
+    } else {
+        // -------------------------------------------------- epilogue
+        const int q = warp & 3;  // TMEM lane quadrant
+        const int half = lane >> 4;
+        int acc = 0;
+        uint32_t aph = 0;
+        pdl_wait();  // the token rows' scales come from the launch before
+        for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
+            const ItemInfo it = decode(item);
+            // output row of this thread, and its scale(s)
+            const int m = MODE == kPhase1 ? it.mt * 64 + q * 16 + (lane & 15) : it.mt * kM + q * 32 + lane;
+            float sw = 0.0f, su = 0.0f;
+            if (MODE == kLinear) {
+                if (m < p.M) sw = __ldg(p.wscale + m);
+            } else {
+                const uint8_t *blob = expert_blob(p.L, it.e);
+                if (blob != nullptr) {
+                    const float *sc =
+                        reinterpret_cast<const float *>(blob + (MODE == kPhase1 ? p.L.off.s13 : p.L.off.s2));
+                    if (m < p.M) sw = __ldg(sc + m);
+                    if (MODE == kPhase1) su = __ldg(sc + p.M + m);
+                }
+            }
+            if (!__all_sync(kAll, mbar_wait(&tfull[acc], aph, &s_abort))) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kNMax);
+            for (int c0 = 0; c0 < it.n; c0 += 16) {
+                float raw[16];
+                tmem_ld16(taddr + (uint32_t)c0, raw);
+                const int cl = c0 + (lane & 15);
+                const float sb = cl < it.n ? __ldg(p.brow + it.row0 + cl) : 0.0f;
+                if (MODE == kPhase1) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        // even column to the gate's lanes, odd column to the up's
+                        const int even = __float_as_int(raw[2 * j]), odd = __float_as_int(raw[2 * j + 1]);
+                        const int own = half ? odd : even;
+                        const int oth = __shfl_xor_sync(kAll, half ? even : odd, 16);
+                        const float s = __shfl_sync(kAll, sb, 2 * j + half);
+                        const int c = c0 + 2 * j + half;
+                        if (c < it.n)
+                            static_cast<float *>(p.out)[(size_t)(it.row0 + c) * p.M + m] =
+                                gate_up(half ? oth : own, half ? own : oth, s, sw, su);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float s = __shfl_sync(kAll, sb, j);
+                        if (c0 + j < it.n && m < p.M) {
+                            const float v = scaled(__float_as_int(raw[j]), s, sw);
+                            const size_t at = (size_t)(it.row0 + c0 + j) * p.M + m;
+                            if (MODE == kPhase2 || p.fp32) static_cast<float *>(p.out)[at] = v;
+                            else static_cast<uint16_t *>(p.out)[at] = f32_to_bf16_rne(v);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[acc]);
+            acc ^= 1;
+            aph ^= acc == 0;
+        }
+    }
+
+    if (s_abort) {
+        // copies and products still in flight end long before this (2 ms)
+        const long long t0 = clock64();
+        while (clock64() - t0 < 4000000ll) {}
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// Token codes and scales into sorted-route order, one warp per row.
+__global__ void __launch_bounds__(256) k_gather_i8(const int8_t *__restrict__ xq, const float *__restrict__ sx,
+                                                   const int32_t *__restrict__ sorted_route,
+                                                   const int32_t *__restrict__ offsets, int E, int k, int H, int R,
+                                                   int8_t *__restrict__ xs, float *__restrict__ ss) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, per = H / 16;
+    const int n = min(__ldg(offsets + E), R);
+    const int warps = (int)(gridDim.x * (blockDim.x >> 5));
+    for (int s = (int)(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)); s < n; s += warps) {
+        const int route = __ldg(sorted_route + s);
+        if (route < 0 || route >= R) {
+            if (lane == 0) record_error(0x2009u, (unsigned)s);
+            continue;
+        }
+        const int t = route / k;
+        const uint4 *src = reinterpret_cast<const uint4 *>(xq + (size_t)t * H);
+        uint4 *dst = reinterpret_cast<uint4 *>(xs + (size_t)s * H);
+        for (int c0 = lane; c0 < per; c0 += 32 * 6) {
+            uint4 u[6];
+#pragma unroll
+            for (int j = 0; j < 6; ++j)
+                if (c0 + 32 * j < per) u[j] = __ldg(src + c0 + 32 * j);
+#pragma unroll
+            for (int j = 0; j < 6; ++j)
+                if (c0 + 32 * j < per) dst[c0 + 32 * j] = u[j];
+        }
+        if (lane == 0) ss[s] = __ldg(sx + t);
+    }
+}
+
+// Codes and scale of each row of h, one warp per row.
+__global__ void __launch_bounds__(256) k_codes_h(const float *__restrict__ h, const int32_t *__restrict__ offsets, int E,
+                                                 int I, int R, int8_t *__restrict__ hq, float *__restrict__ sh) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, n = min(__ldg(offsets + E), R);
+    const int warps = (int)(gridDim.x * (blockDim.x >> 5));
+    for (int s = (int)(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)); s < n; s += warps) {
+        const float4 *src = reinterpret_cast<const float4 *>(h + (size_t)s * I);
+        float amax = 0.0f;
+        for (int c = lane; c < I / 4; c += 32) {
+            const float4 v = src[c];
+            amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
+        const float sc = __fdiv_rn(amax, 127.0f);
+        for (int c = lane; c < I / 4; c += 32) {
+            const float4 v = src[c];
+            reinterpret_cast<uint32_t *>(hq + (size_t)s * I)[c] =
+                ((uint32_t)code_i8(v.x, sc) & 0xffu) | (((uint32_t)code_i8(v.y, sc) & 0xffu) << 8) |
+                (((uint32_t)code_i8(v.z, sc) & 0xffu) << 16) | (((uint32_t)code_i8(v.w, sc) & 0xffu) << 24);
+        }
+        if (lane == 0) sh[s] = sc;
+    }
+}
+
+// ------------------------------------------------------------------ host side
+constexpr size_t kDynSmem = 1024 + kRing;
+static_assert(kDynSmem + 4 * (3 * kMaxE + 1) + 2 * kMaxE + 512 <= 232448, "int8 tensor-core kernel exceeds shared memory");
+
+// W13 codes of every blob: {K, 16 rows, blocks of 16 rows, gate or up, blob},
+// box = 16 gate rows and their 16 up rows.
+bool encode_w13(CUtensorMap *m, const void *base, uint64_t H, uint64_t I, uint64_t blobs, uint64_t stride) {
+    cuuint64_t dims[5] = {H, 16, I / 16, 2, blobs};
+    cuuint64_t strides[4] = {H, 16 * H, I * H, stride};
+    cuuint32_t box[5] = {(cuuint32_t)kKB, 16, 1, 2, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE>
+cudaError_t launch_tc(const CUtensorMap &mh, const CUtensorMap &mp, const void *b, const TcI8Params &p, int n_sm,
+                      cudaStream_t s) {
+    CUtensorMap b16, b32;
+    if (!encode_2d(&b16, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)p.K, (uint64_t)p.R, kKB, 16,
+                   CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&b32, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)p.K, (uint64_t)p.R, kKB, 32,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    auto kern = k_i8_tc<MODE>;
+    static bool attr[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!attr[dev]) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDynSmem);
+        if (err != cudaSuccess) return err;
+        attr[dev] = true;
+    }
+    return launch_pdl(kern, dim3((unsigned)n_sm), dim3(kThreads), kDynSmem, s, mh, mp, b16, b32, p);
+}
+
+size_t a256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+cudaError_t launch_linear_i8_tc(const LinearArgs &a, cudaStream_t s) {
+    cudaError_t err = get_encoder();
+    int n_sm = 0;
+    if (err != cudaSuccess || (err = sm_count(&n_sm)) != cudaSuccess) return err;
+    CUtensorMap mw;
+    if (!encode_3d(&mw, a.wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N, 1,
+                   (uint64_t)a.K, kKB, kM, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    TcI8Params p{};
+    p.E = 1;
+    p.R = a.T;
+    p.K = a.K;
+    p.M = a.N;
+    p.brow = a.sx;
+    p.wscale = a.sw;
+    p.out = a.y;
+    p.fp32 = a.fp32;
+    return launch_tc<kLinear>(mw, mw, a.xq, p, n_sm, s);
+}
+
+// h fp32 | codes of h | scales of h | gathered codes | gathered scales
+size_t ffn_i8_tc_workspace(int H, int I, int T, int k) {
+    const size_t R = (size_t)T * k;
+    return a256(R * I * 4) + a256(R * I) + a256(R * 4) + a256(R * H) + a256(R * 4);
+}
+
+cudaError_t launch_ffn_i8_tc(const FfnI8Args &a, cudaStream_t s) {
+    cudaError_t err = get_encoder();
+    int n_sm = 0;
+    if (err != cudaSuccess || (err = sm_count(&n_sm)) != cudaSuccess) return err;
+    const int R = a.T * a.k, H = a.L.H, I = a.L.I, E = a.L.E;
+    char *at = static_cast<char *>(a.ws);
+    float *h = reinterpret_cast<float *>(at);
+    at += a256((size_t)R * I * 4);
+    int8_t *hq = reinterpret_cast<int8_t *>(at);
+    at += a256((size_t)R * I);
+    float *sh = reinterpret_cast<float *>(at);
+    at += a256((size_t)R * 4);
+    int8_t *xs = reinterpret_cast<int8_t *>(at);
+    at += a256((size_t)R * H);
+    float *ss = reinterpret_cast<float *>(at);
+
+    const bool slotted = a.L.slot_table != nullptr;
+    const uint8_t *pool = slotted ? a.L.pool : a.L.home;
+    const uint64_t slots = slotted ? (uint64_t)a.L.pool_slots : (uint64_t)E;
+    CUtensorMap h1, p1, h2, p2;
+    if (!encode_w13(&h1, a.L.home + a.L.off.q13, H, I, E, a.L.stride) ||
+        !encode_w13(&p1, pool + a.L.off.q13, H, I, slots, a.L.stride) ||
+        !encode_3d(&h2, a.L.home + a.L.off.q2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, I, H, E, a.L.stride, kKB, kM,
+                   CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_3d(&p2, pool + a.L.off.q2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, I, H, slots, a.L.stride, kKB, kM,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+
+    const int blocks = (int)std::min<int64_t>(((int64_t)R + 7) / 8, (int64_t)n_sm * 8);
+    err = launch_pdl(k_gather_i8, dim3((unsigned)blocks), dim3(256), 0, s, a.xq, a.sx, a.sorted_route, a.offsets, E, a.k,
+                     H, R, xs, ss);
+    if (err != cudaSuccess) return err;
+    TcI8Params p{};
+    p.L = a.L;
+    p.counts = a.counts;
+    p.offsets = a.offsets;
+    p.E = E;
+    p.R = R;
+    p.K = H;
+    p.M = I;
+    p.brow = ss;
+    p.out = h;
+    if ((err = launch_tc<kPhase1>(h1, p1, xs, p, n_sm, s)) != cudaSuccess) return err;
+    err = launch_pdl(k_codes_h, dim3((unsigned)blocks), dim3(256), 0, s, (const float *)h, a.offsets, E, I, R, hq, sh);
+    if (err != cudaSuccess) return err;
+    p.K = I;
+    p.M = H;
+    p.brow = sh;
+    p.out = a.rows;
+    return launch_tc<kPhase2>(h2, p2, hq, p, n_sm, s);
+}
+
+cudaError_t i8tc_take_error(unsigned *code, unsigned *info) {
+    unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_i8tc_error, sizeof(unsigned));
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(info, g_i8tc_error_info, sizeof(unsigned));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_i8tc_error, &zero, sizeof(unsigned));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_i8tc_error_info, &zero, sizeof(unsigned));
+    return e;
+}
+
+}  // namespace moe

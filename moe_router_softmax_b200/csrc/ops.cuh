@@ -36,7 +36,7 @@ struct NormArgs {
 };
 cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t s);
 
-// int8 x int8 products (i8_gemv.cu).
+// int8 x int8 products (i8_gemv.cu: few tokens; i8_tc.cu: tensor cores).
 struct LinearArgs {
     const int8_t *xq, *wq;  // [T][K], [N][K]
     const float *sx, *sw;   // [T], [N]
@@ -45,8 +45,9 @@ struct LinearArgs {
     int fp32;
 };
 cudaError_t launch_linear_i8(const LinearArgs &a, cudaStream_t s);
+cudaError_t launch_linear_i8_tc(const LinearArgs &a, cudaStream_t s);
 
-// Grouped FFN with int8 activations over int8 experts (i8_gemv.cu).
+// Grouped FFN with int8 activations over int8 experts (same files).
 struct FfnI8Args {
     LayerView L;
     const int8_t *xq;  // [T][H]
@@ -56,13 +57,23 @@ struct FfnI8Args {
     float *rows;       // [T k][H], sorted order
     void *ws;
 };
-size_t ffn_i8_workspace(int E, int H, int I, int T, int k);
+size_t ffn_i8_workspace(int H, int I, int T, int k);  // of whichever kernels take the call
 cudaError_t launch_ffn_i8(const FfnI8Args &a, cudaStream_t s);
+size_t ffn_i8_tc_workspace(int H, int I, int T, int k);
+cudaError_t launch_ffn_i8_tc(const FfnI8Args &a, cudaStream_t s);
 cudaError_t i8_take_error(unsigned *code, unsigned *info);
+cudaError_t i8tc_take_error(unsigned *code, unsigned *info);
 
-__device__ __forceinline__ float gelu_tanh_f(float v) {
-    const float u = 0.7978845608028654f * (v + 0.044715f * v * v * v);  // sqrt(2/pi)
-    return 0.5f * v * (1.0f + tanhf(u));
+// The scales' products and the gate, in a fixed order of roundings: every kernel
+// that takes a shape gives the same bits.
+__device__ __forceinline__ float scaled(int sum, float s_token, float s_row) {
+    return __fmul_rn(__fmul_rn((float)sum, s_token), s_row);
+}
+__device__ __forceinline__ float gate_up(int g_sum, int u_sum, float s_token, float s_gate, float s_up) {
+    const float v = scaled(g_sum, s_token, s_gate), u = scaled(u_sum, s_token, s_up);
+    const float cube = __fmul_rn(__fmul_rn(v, v), v);
+    const float t = tanhf(__fmul_rn(0.7978845608028654f, __fmaf_rn(0.044715f, cube, v)));  // sqrt(2/pi)
+    return __fmul_rn(__fmul_rn(__fmul_rn(0.5f, v), __fadd_rn(1.0f, t)), u);
 }
 
 // int8 code of v at scale s (moe_quantize_int8's steps); 0 at s = 0 and for a NaN.
