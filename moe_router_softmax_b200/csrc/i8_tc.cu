@@ -24,6 +24,8 @@
 // token rows), its depth set by the launch's largest block; two accumulators of 256
 // columns, so that an item's epilogue overlaps the next item's products.  Every
 // wait is bounded: on a timeout the kernel records it and every role drains out.
+#include <cuda_bf16.h>
+
 #include <algorithm>
 
 #include "ops.cuh"
@@ -39,14 +41,14 @@ constexpr int kM = 128;                        // weight rows per tile
 constexpr int kKB = 128;                       // codes of K per stage: one swizzle row
 constexpr int kNMax = 256;                     // tokens per block
 constexpr uint32_t kABytes = kM * kKB;         // 16 KB
-constexpr int kRing = 205 * 1024;
+constexpr int kRing = 204 * 1024;
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 4;
 constexpr int kWarpB = 2 + kEpiWarps;
 constexpr int kThreads = 32 * (kWarpB + 1);
 constexpr int kTmemCols = 512;
 
-enum { kLinear = 0, kPhase1 = 1, kPhase2 = 2 };
+enum { kLinear = 0, kLinearF32 = 1, kPhase1 = 2, kPhase2 = 3 };
 
 // First problem a kernel of this file recorded (0 = none), read and cleared by
 // moe_take_device_errors(): 0x1000 | warp for a wait that gave up, 0x2006 a slot
@@ -71,7 +73,6 @@ struct TcI8Params {
     const float *brow;               // scale per token row
     const float *wscale;             // linear: scale per output row
     void *out;                       // y, h or rows
-    int fp32;                        // linear: y in fp32
 };
 
 __device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -122,6 +123,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+    __shared__ __align__(16) float s_scale[kEpiWarps][kNMax];  // scales of the item's token rows, a copy per epilogue warp
 
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -147,7 +149,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     // dense: one expert that holds every token.  phases: the experts with routes
-    if (MODE != kLinear) {
+    if (MODE >= kPhase1) {
         for (int e = threadIdx.x; e < p.E; e += blockDim.x) s_cnt[e] = __ldg(p.counts + e);
         __syncthreads();
     }
@@ -155,8 +157,8 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         int n_act = 0, run = 0, rows = 16;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
-            const int n = e < p.E ? (MODE == kLinear ? p.R : s_cnt[e]) : 0;
-            const int off = MODE == kLinear || e >= p.E ? 0 : __ldg(p.offsets + e);
+            const int n = e < p.E ? (MODE < kPhase1 ? p.R : s_cnt[e]) : 0;
+            const int off = MODE < kPhase1 || e >= p.E ? 0 : __ldg(p.offsets + e);
             __syncwarp();  // every lane has read its count before any is written in place
             const bool act = n > 0;
             const unsigned m = __ballot_sync(kAll, act);
@@ -208,7 +210,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         r.row0 = s_row0[lo] + nb * blk;
         r.n = min(blk, n_e - nb * blk);
         r.n_mma = (max(r.n, 1) + 15) & ~15;
-        if (MODE != kLinear) {
+        if (MODE >= kPhase1) {
             bool bad;
             expert_slot(p.L, r.e, &bad);
             if (bad) record_error(0x2006u, (unsigned)__ldg(p.L.slot_table + r.e));
@@ -231,15 +233,15 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             // The dense product's weights may come from the launch before; the
             // phases' launches follow this library's own (gather, codes of h),
             // which have waited for all before them and write no weights.
-            if (MODE == kLinear) pdl_wait();
-            const uint64_t pol = MODE == kLinear ? l2_policy_last() : l2_policy_first();
+            if (MODE < kPhase1) pdl_wait();
+            const uint64_t pol = MODE < kPhase1 ? l2_policy_last() : l2_policy_first();
             int st = 0;
             uint32_t ph = 0;
             for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
                 const ItemInfo it = decode(item);
                 const CUtensorMap *ma = &map_home;
                 int z = 0;
-                if (MODE != kLinear) {
+                if (MODE >= kPhase1) {
                     bool bad;
                     const int s = expert_slot(p.L, it.e, &bad);
                     if (s >= 0) ma = &map_pool;
@@ -331,7 +333,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             // output row of this thread, and its scale(s)
             const int m = MODE == kPhase1 ? it.mt * 64 + q * 16 + (lane & 15) : it.mt * kM + q * 32 + lane;
             float sw = 0.0f, su = 0.0f;
-            if (MODE == kLinear) {
+            if (MODE < kPhase1) {
                 if (m < p.M) sw = __ldg(p.wscale + m);
             } else {
                 const uint8_t *blob = expert_blob(p.L, it.e);
@@ -342,37 +344,51 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                     if (MODE == kPhase1) su = __ldg(sc + p.M + m);
                 }
             }
+            float *sb = s_scale[warp - 2];
+            for (int c = lane; c < kNMax; c += 32)
+                if (c < it.n_mma) sb[c] = c < it.n ? __ldg(p.brow + it.row0 + c) : 0.0f;
+            __syncwarp();
             if (!__all_sync(kAll, mbar_wait(&tfull[acc], aph, &s_abort))) break;
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kNMax);
-            for (int c0 = 0; c0 < it.n; c0 += 16) {
-                float raw[16];
-                tmem_ld16(taddr + (uint32_t)c0, raw);
-                const int cl = c0 + (lane & 15);
-                const float sb = cl < it.n ? __ldg(p.brow + it.row0 + cl) : 0.0f;
+            for (int c0 = 0; c0 < it.n; c0 += 32) {
+                int raw[32];
+                tmem_ld32(taddr + (uint32_t)c0, raw);
                 if (MODE == kPhase1) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        // even column to the gate's lanes, odd column to the up's
-                        const int even = __float_as_int(raw[2 * j]), odd = __float_as_int(raw[2 * j + 1]);
-                        const int own = half ? odd : even;
-                        const int oth = __shfl_xor_sync(kAll, half ? even : odd, 16);
-                        const float s = __shfl_sync(kAll, sb, 2 * j + half);
-                        const int c = c0 + 2 * j + half;
-                        if (c < it.n)
-                            static_cast<float *>(p.out)[(size_t)(it.row0 + c) * p.M + m] =
-                                gate_up(half ? oth : own, half ? own : oth, s, sw, su);
-                    }
-                } else {
+                    // even columns to the gates' lanes, odd columns to the ups'
+                    float v[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float s = __shfl_sync(kAll, sb, j);
-                        if (c0 + j < it.n && m < p.M) {
-                            const float v = scaled(__float_as_int(raw[j]), s, sw);
-                            const size_t at = (size_t)(it.row0 + c0 + j) * p.M + m;
-                            if (MODE == kPhase2 || p.fp32) static_cast<float *>(p.out)[at] = v;
-                            else static_cast<uint16_t *>(p.out)[at] = f32_to_bf16_rne(v);
-                        }
+                        const int own = half ? raw[2 * j + 1] : raw[2 * j];
+                        const int oth = __shfl_xor_sync(kAll, half ? raw[2 * j] : raw[2 * j + 1], 16);
+                        const float2 s2 = *reinterpret_cast<const float2 *>(sb + c0 + 2 * j);
+                        v[j] = gate_up(half ? oth : own, half ? own : oth, half ? s2.y : s2.x, sw, su);
+                    }
+                    float *o = static_cast<float *>(p.out) + (size_t)(it.row0 + c0 + half) * p.M + m;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c0 + half + 2 * j < it.n) o[(size_t)(2 * j) * p.M] = v[j];
+                } else {
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 s4 = *reinterpret_cast<const float4 *>(sb + c0 + j);
+                        v[j] = scaled(raw[j], s4.x, sw);
+                        v[j + 1] = scaled(raw[j + 1], s4.y, sw);
+                        v[j + 2] = scaled(raw[j + 2], s4.z, sw);
+                        v[j + 3] = scaled(raw[j + 3], s4.w, sw);
+                    }
+                    const size_t at = (size_t)(it.row0 + c0) * p.M + m;
+                    if (MODE == kLinear) {
+                        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + at;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c0 + j < it.n && m < p.M) o[(size_t)j * p.M] = __float2bfloat16_rn(v[j]);
+                    } else {
+                        float *o = static_cast<float *>(p.out) + at;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c0 + j < it.n && m < p.M) o[(size_t)j * p.M] = v[j];
                     }
                 }
             }
@@ -458,7 +474,7 @@ __global__ void __launch_bounds__(256) k_codes_h(const float *__restrict__ h, co
 
 // ------------------------------------------------------------------ host side
 constexpr size_t kDynSmem = 1024 + kRing;
-static_assert(kDynSmem + 4 * (3 * kMaxE + 1) + 2 * kMaxE + 512 <= 232448, "int8 tensor-core kernel exceeds shared memory");
+static_assert(kDynSmem + 4 * (3 * kMaxE + 1) + 2 * kMaxE + 4 * kEpiWarps * kNMax + 512 <= 232448, "int8 tensor-core kernel exceeds shared memory");
 
 // W13 codes of every blob: {K, 16 rows, blocks of 16 rows, gate or up, blob},
 // box = 16 gate rows and their 16 up rows.
@@ -515,8 +531,7 @@ cudaError_t launch_linear_i8_tc(const LinearArgs &a, cudaStream_t s) {
     p.brow = a.sx;
     p.wscale = a.sw;
     p.out = a.y;
-    p.fp32 = a.fp32;
-    return launch_tc<kLinear>(mw, mw, a.xq, p, n_sm, s);
+    return a.fp32 ? launch_tc<kLinearF32>(mw, mw, a.xq, p, n_sm, s) : launch_tc<kLinear>(mw, mw, a.xq, p, n_sm, s);
 }
 
 // h fp32 | codes of h | scales of h | gathered codes | gathered scales
