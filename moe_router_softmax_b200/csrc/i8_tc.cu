@@ -100,8 +100,8 @@ struct Items {
 
 // Blocks of an expert's n routes: as few as kNMax allows, of even size, a
 // multiple of 16 (the MMA's N).
-__device__ __forceinline__ int blocks_of(int n) { return (n + kNMax - 1) / kNMax; }
-__device__ __forceinline__ int block_rows(int n) {
+__host__ __device__ __forceinline__ int blocks_of(int n) { return (n + kNMax - 1) / kNMax; }
+__host__ __device__ __forceinline__ int block_rows(int n) {
     const int nb = blocks_of(n);
     return ((n + nb - 1) / nb + 15) & ~15;
 }
@@ -113,7 +113,7 @@ struct ItemInfo {
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CUtensorMap map_pool,
-        const __grid_constant__ CUtensorMap map_b16, const __grid_constant__ CUtensorMap map_b32, const TcI8Params p) {
+        const __grid_constant__ CUtensorMap map_b16, const __grid_constant__ CUtensorMap map_big, const TcI8Params p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ int s_base[kMaxE + 1];     // first item of each active expert
     __shared__ int s_row0[kMaxE];
@@ -182,10 +182,8 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         }
         rows = (int)__reduce_max_sync(kAll, (unsigned)rows);
         if (lane == 0) {
-            // blocks over 32 rows are loaded in boxes of 32
-            const int b_rows = rows <= 32 ? rows : (rows + 31) & ~31;
             s_base[n_act] = run;
-            s_items = Items{n_act, run, m_tiles, b_rows, min(kMaxStages, kRing / ((int)kABytes + b_rows * kKB))};
+            s_items = Items{n_act, run, m_tiles, rows, min(kMaxStages, kRing / ((int)kABytes + rows * kKB))};
         }
     }
     tc_fence_before();
@@ -273,16 +271,20 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             uint32_t ph = 0;
             for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
                 const ItemInfo it = decode(item);
-                const int box = it.n_mma > 32 ? 32 : 16;
-                const int rows = (it.n_mma + box - 1) & ~(box - 1);  // rows past the block are read, not used
+                // dense: the whole block in one box (rows past the last token read as
+                // zeros); phases: boxes of 64 rows, then of 16
+                const int rows = MODE < kPhase1 ? s_items.b_rows : it.n_mma;
+                const int big = MODE < kPhase1 ? rows : 64;
                 bool ok = true;
                 for (int kk = 0; kk < nk; ++kk) {
                     if (!mbar_wait(&empty[st], ph ^ 1, &s_abort)) { ok = false; break; }
                     mbar_arrive_expect_tx(&full[st], (uint32_t)rows * kKB);
                     uint8_t *dst = ring + st * stage_bytes + kABytes;
-                    for (int j = 0; j < rows; j += box)
-                        tma_load_2d(dst + j * kKB, box == 32 ? &map_b32 : &map_b16, &full[st], kk * kKB, it.row0 + j,
-                                    pol);
+                    int j = 0;
+                    for (; j + big <= rows; j += big)
+                        tma_load_2d(dst + j * kKB, &map_big, &full[st], kk * kKB, it.row0 + j, pol);
+                    for (; j < rows; j += 16)
+                        tma_load_2d(dst + j * kKB, &map_b16, &full[st], kk * kKB, it.row0 + j, pol);
                     if (++st == S) { st = 0; ph ^= 1; }
                 }
                 if (!ok) break;
@@ -307,11 +309,18 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                     tc_fence_after();
                     const uint32_t sa = smem_u32(ring + st * stage_bytes);
                     const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + kABytes);
-                    // 32 codes of K per MMA: 32 bytes, 2 in the descriptor's address field;
-                    // past K both operands hold zeros
-                    const int steps = min(kKB / 32, (p.K - kk * kKB + 31) / 32);
-                    for (int j = 0; j < steps; ++j)
-                        tc_mma_i8(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (kk | j) != 0);
+                    // 32 codes of K per MMA: 32 bytes, 2 in the descriptor's address field.
+                    // The four of a whole stage are unrolled: 128 cycles each at N = 256 (the
+                    // tensor pipe's), where a counted loop took 144 to issue one
+                    if ((kk + 1) * kKB <= p.K) {
+#pragma unroll
+                        for (int j = 0; j < kKB / 32; ++j)
+                            tc_mma_i8(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (kk | j) != 0);
+                    } else {
+                        const int steps = (p.K - kk * kKB + 31) / 32;  // past K both operands hold zeros
+                        for (int j = 0; j < steps; ++j)
+                            tc_mma_i8(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (kk | j) != 0);
+                    }
                     tc_commit(&empty[st]);
                     if (++st == S) { st = 0; ph ^= 1; }
                 }
@@ -491,10 +500,12 @@ bool encode_w13(CUtensorMap *m, const void *base, uint64_t H, uint64_t I, uint64
 template <int MODE>
 cudaError_t launch_tc(const CUtensorMap &mh, const CUtensorMap &mp, const void *b, const TcI8Params &p, int n_sm,
                       cudaStream_t s) {
-    CUtensorMap b16, b32;
+    CUtensorMap b16, big;
+    // dense: the block that the kernel will take; phases: 64 rows
+    const int big_rows = MODE < kPhase1 ? block_rows(p.R) : 64;
     if (!encode_2d(&b16, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)p.K, (uint64_t)p.R, kKB, 16,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_2d(&b32, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)p.K, (uint64_t)p.R, kKB, 32,
+        !encode_2d(&big, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)p.K, (uint64_t)p.R, kKB, (uint32_t)big_rows,
                    CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     auto kern = k_i8_tc<MODE>;
@@ -508,7 +519,7 @@ cudaError_t launch_tc(const CUtensorMap &mh, const CUtensorMap &mp, const void *
         if (err != cudaSuccess) return err;
         attr[dev] = true;
     }
-    return launch_pdl(kern, dim3((unsigned)n_sm), dim3(kThreads), kDynSmem, s, mh, mp, b16, b32, p);
+    return launch_pdl(kern, dim3((unsigned)n_sm), dim3(kThreads), kDynSmem, s, mh, mp, b16, big, p);
 }
 
 size_t a256(size_t n) { return (n + 255) & ~(size_t)255; }
