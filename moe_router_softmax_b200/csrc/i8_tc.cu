@@ -18,8 +18,8 @@
 //   phase 2  as linear, per expert, over the codes of h; rows[s][m] = D sh[s] s2[m]
 //
 // Persistent CTAs, one per SM; warp 0 TMA producer of the weights, warp 1 TMEM
-// allocation and the MMA issuer, warps 2..5 epilogue (TMEM -> registers ->
-// global; warp w reads lanes 32 (w % 4) ..), warp 6 TMA producer of the tokens.
+// allocation and the MMA issuer, warps 2..9 epilogue (TMEM -> registers ->
+// global; warp w reads lanes 32 (w % 4) ..), warp 10 TMA producer of the tokens.
 // One ring of stages of 128 codes of K (a stage: 128 weight rows and one block of
 // token rows), its depth set by the launch's largest block; two accumulators of 256
 // columns, so that an item's epilogue overlaps the next item's products.  Every
@@ -41,9 +41,9 @@ constexpr int kM = 128;                        // weight rows per tile
 constexpr int kKB = 128;                       // codes of K per stage: one swizzle row
 constexpr int kNMax = 256;                     // tokens per block
 constexpr uint32_t kABytes = kM * kKB;         // 16 KB
-constexpr int kRing = 204 * 1024;
+constexpr int kRing = 200 * 1024;
 constexpr int kMaxStages = 12;
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;                   // two per TMEM quadrant
 constexpr int kWarpB = 2 + kEpiWarps;
 constexpr int kThreads = 32 * (kWarpB + 1);
 constexpr int kTmemCols = 512;
@@ -332,7 +332,8 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         }
     } else {
         // -------------------------------------------------- epilogue
-        const int q = warp & 3;  // TMEM lane quadrant
+        const int q = warp & 3;         // TMEM lane quadrant
+        const int eh = (warp - 2) >> 2;  // which of its two warps: they take every other 32 columns
         const int half = lane >> 4;
         int acc = 0;
         uint32_t aph = 0;
@@ -360,7 +361,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             if (!__all_sync(kAll, mbar_wait(&tfull[acc], aph, &s_abort))) break;
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kNMax);
-            for (int c0 = 0; c0 < it.n; c0 += 32) {
+            for (int c0 = 32 * eh; c0 < it.n; c0 += 64) {
                 int raw[32];
                 tmem_ld32(taddr + (uint32_t)c0, raw);
                 if (MODE == kPhase1) {
