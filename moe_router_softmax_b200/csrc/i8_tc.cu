@@ -75,13 +75,22 @@ struct TcI8Params {
     void *out;                       // y, h or rows
 };
 
+// Called by a whole warp; one lane issues.
 __device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_warp(uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
 // {x, row, 16-row block, gate or up, blob} box of W13.
@@ -292,43 +301,47 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         }
     } else if (warp == 1) {
         // -------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            int st = 0, acc = 0;
-            uint32_t ph = 0, aph = 0;
-            for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
-                const ItemInfo it = decode(item);
-                if (!mbar_wait(&tempty[acc], aph ^ 1, &s_abort)) break;
+        // The whole warp walks the stages and an elected lane issues, so that the
+        // descriptors stay in uniform registers.  A wait on a completed phase costs
+        // ~130 cycles: the next stage's is tested before this one's products are issued.
+        int st = 0, acc = 0;
+        uint32_t ph = 0, aph = 0;
+        bool ready = false;
+        const uint64_t desc0 = sw128_desc(smem_u32(ring));
+        for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
+            const ItemInfo it = decode(item);
+            if (!__all_sync(kAll, mbar_wait(&tempty[acc], aph ^ 1, &s_abort))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + (uint32_t)(acc * kNMax);
+            // int32 sums, both operands signed 8-bit, N and M of the tile
+            const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(it.n_mma >> 3) << 17) |
+                                   ((uint32_t)(kM >> 4) << 24);
+            bool ok = true;
+            for (int kk = 0; kk < nk; ++kk) {
+                if (!__all_sync(kAll, ready) && !__all_sync(kAll, mbar_wait(&full[st], ph, &s_abort))) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * kNMax);
-                // int32 sums, both operands signed 8-bit, N and M of the tile
-                const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(it.n_mma >> 3) << 17) |
-                                       ((uint32_t)(kM >> 4) << 24);
-                bool ok = true;
-                for (int kk = 0; kk < nk; ++kk) {
-                    if (!mbar_wait(&full[st], ph, &s_abort)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(ring + st * stage_bytes);
-                    const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + kABytes);
-                    // 32 codes of K per MMA: 32 bytes, 2 in the descriptor's address field.
-                    // The four of a whole stage are unrolled: 128 cycles each at N = 256 (the
-                    // tensor pipe's), where a counted loop took 144 to issue one
-                    if ((kk + 1) * kKB <= p.K) {
+                const uint64_t ad = desc0 + (uint64_t)((st * stage_bytes) >> 4), bd = ad + (kABytes >> 4);
+                uint64_t *done = &empty[st];
+                if (++st == S) { st = 0; ph ^= 1; }
+                ready = mbar_test_wait(&full[st], ph);
+                // 32 codes of K per MMA: 32 bytes, 2 in the descriptor's address field.
+                // The four of a whole stage are unrolled: 128 cycles each at N = 256 (the
+                // tensor pipe's), where a counted loop took 144 to issue one
+                if ((kk + 1) * kKB <= p.K) {
 #pragma unroll
-                        for (int j = 0; j < kKB / 32; ++j)
-                            tc_mma_i8(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (kk | j) != 0);
-                    } else {
-                        const int steps = (p.K - kk * kKB + 31) / 32;  // past K both operands hold zeros
-                        for (int j = 0; j < steps; ++j)
-                            tc_mma_i8(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (kk | j) != 0);
-                    }
-                    tc_commit(&empty[st]);
-                    if (++st == S) { st = 0; ph ^= 1; }
+                    for (int j = 0; j < kKB / 32; ++j)
+                        tc_mma_i8(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (kk | j) != 0);
+                } else {
+                    const int steps = (p.K - kk * kKB + 31) / 32;  // past K both operands hold zeros
+                    for (int j = 0; j < steps; ++j)
+                        tc_mma_i8(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (kk | j) != 0);
                 }
-                if (!ok) break;
-                tc_commit(&tfull[acc]);
-                acc ^= 1;
-                aph ^= acc == 0;
+                tc_commit_warp(done);
             }
+            if (!ok) break;
+            tc_commit_warp(&tfull[acc]);
+            acc ^= 1;
+            aph ^= acc == 0;
         }
     } else {
         // -------------------------------------------------- epilogue
