@@ -8,6 +8,7 @@
 //
 // A weight row is read once, 16 bytes per lane, so the weights' bytes bound
 // these kernels.
+#include "i8_math.cuh"
 #include "ops.cuh"
 
 namespace moe {
@@ -137,14 +138,14 @@ __global__ void __launch_bounds__(32 * kWarps) k_ffn_i8_gemv2(const FfnI8Args a,
     const float *hr = h + (size_t)s * I;
     float amax = 0.0f;
     for (int i = threadIdx.x; i < I; i += 32 * kWarps) amax = fmaxf(amax, fabsf(hr[i]));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
+    amax = warp_max(amax);
     if (lane == 0) s_part[warp] = amax;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_part[w]);
-    const float sh = __fdiv_rn(amax, 127.0f);
-    for (int i = threadIdx.x; i < I; i += 32 * kWarps) s_hq[i] = (int8_t)code_i8(hr[i], sh);
+    const CodeScale sc = code_scale(amax);
+    const float sh = sc.s;
+    for (int i = threadIdx.x; i < I; i += 32 * kWarps) s_hq[i] = (int8_t)sc.code(hr[i]);
     __syncthreads();
     const float *s2 = reinterpret_cast<const float *>(blob + a.L.off.s2);
     for (int n = n0 + warp; n < n0 + kRows2; n += kWarps) {

@@ -1,0 +1,49 @@
+// i8_math.cuh -- device arithmetic shared by the int8 kernels: the scales'
+// products, the gate, and the codes of a row.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// The scales' products and the gate, in a fixed order of roundings: every kernel
+// that takes a shape gives the same bits.
+__device__ __forceinline__ float scaled(int sum, float s_token, float s_row) {
+    return __fmul_rn(__fmul_rn((float)sum, s_token), s_row);
+}
+__device__ __forceinline__ float gate_up(int g_sum, int u_sum, float s_token, float s_gate, float s_up) {
+    const float v = scaled(g_sum, s_token, s_gate), u = scaled(u_sum, s_token, s_up);
+    const float cube = __fmul_rn(__fmul_rn(v, v), v);
+    const float t = tanhf(__fmul_rn(0.7978845608028654f, __fmaf_rn(0.044715f, cube, v)));  // sqrt(2/pi)
+    return __fmul_rn(__fmul_rn(__fmul_rn(0.5f, v), __fadd_rn(1.0f, t)), u);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+// Scale of a row from its largest magnitude, and the codes at it: rint(v / s) by a
+// multiplication with 1 / s (a division per value costs more than the rest of a code),
+// clamped to +-127; 0 where s is 0 and for a NaN.  Where 1 / s overflows (s below
+// 2^-128), v / s itself.
+struct CodeScale {
+    float s, inv;
+    __device__ __forceinline__ int code(float v) const {
+        const float q = inv <= 3.402823466e+38f ? __fmul_rn(v, inv) : __fdiv_rn(v, s);
+        return max(-127, min(127, __float2int_rn(q)));
+    }
+    __device__ __forceinline__ uint32_t code4(float4 v) const {
+        return ((uint32_t)code(v.x) & 0xffu) | (((uint32_t)code(v.y) & 0xffu) << 8) |
+               (((uint32_t)code(v.z) & 0xffu) << 16) | (((uint32_t)code(v.w) & 0xffu) << 24);
+    }
+};
+__device__ __forceinline__ CodeScale code_scale(float amax) {
+    CodeScale c;
+    c.s = __fdiv_rn(amax, 127.0f);
+    c.inv = c.s != 0.0f ? __fdiv_rn(1.0f, c.s) : 0.0f;
+    return c;
+}
+
+}  // namespace moe

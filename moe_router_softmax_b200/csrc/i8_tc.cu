@@ -20,14 +20,16 @@
 // Persistent CTAs, one per SM; warp 0 TMA producer of the weights, warp 1 TMEM
 // allocation and the MMA issuer, warps 2..9 epilogue (TMEM -> registers ->
 // global; warp w reads lanes 32 (w % 4) ..), warp 10 TMA producer of the tokens.
-// One ring of stages of 128 codes of K (a stage: 128 weight rows and one block of
-// token rows), its depth set by the launch's largest block; two accumulators of 256
-// columns, so that an item's epilogue overlaps the next item's products.  Every
+// Two rings of stages of 128 codes of K, one of weight tiles and one of token blocks,
+// whose slots share the CTA's memory by the launch's largest block: the weights come
+// from HBM and want many stages in flight, the tokens from L2.  Two accumulators of
+// 256 columns, so that an item's epilogue overlaps the next item's products.  Every
 // wait is bounded: on a timeout the kernel records it and every role drains out.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 
+#include "i8_math.cuh"
 #include "ops.cuh"
 #include "tc_ptx.cuh"
 
@@ -41,8 +43,8 @@ constexpr int kM = 128;                        // weight rows per tile
 constexpr int kKB = 128;                       // codes of K per stage: one swizzle row
 constexpr int kNMax = 256;                     // tokens per block
 constexpr uint32_t kABytes = kM * kKB;         // 16 KB
-constexpr int kRing = 200 * 1024;
-constexpr int kMaxStages = 12;
+constexpr int kRing = 198 * 1024;
+constexpr int kMaxStages = 12;                 // of either ring
 constexpr int kEpiWarps = 8;                   // two per TMEM quadrant
 constexpr int kWarpB = 2 + kEpiWarps;
 constexpr int kThreads = 32 * (kWarpB + 1);
@@ -104,8 +106,20 @@ __device__ __forceinline__ void tma_load_5d(void *smem_dst, const CUtensorMap *m
 }
 
 struct Items {
-    int n_act, total, m_tiles, b_rows, stages;
+    int n_act, total, b_rows, a_slots, b_slots;
 };
+
+// Slots of the two rings for token blocks of `rows` rows.  The dense product's
+// operands both come from L2 and get the same number.  So do the phases' up to 64
+// rows; above, three token slots leave the rest of the memory to the weights.
+template <int MODE>
+__device__ __forceinline__ void split_ring(int rows, Items *it) {
+    const int b = rows * kKB;
+    const int even = min(kMaxStages, kRing / ((int)kABytes + b));
+    it->b_rows = rows;
+    it->b_slots = MODE < kPhase1 || rows <= 64 ? even : 3;
+    it->a_slots = MODE < kPhase1 ? even : min(kMaxStages, (kRing - it->b_slots * b) / (int)kABytes);
+}
 
 // Blocks of an expert's n routes: as few as kNMax allows, of even size, a
 // multiple of 16 (the MMA's N).
@@ -115,8 +129,25 @@ __host__ __device__ __forceinline__ int block_rows(int n) {
     return ((n + nb - 1) / nb + 15) & ~15;
 }
 
+// Up to 32 columns of one output row, `stride` values apart (whole chunks without
+// a check per column).
+__device__ __forceinline__ void put(float *o, float v) { *o = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *o, float v) { *o = __float2bfloat16_rn(v); }
+template <class T>
+__device__ __forceinline__ void store_cols(T *o, int stride, const float v[32], int n) {
+    if (n >= 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) put(o + (size_t)j * stride, v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < n) put(o + (size_t)j * stride, v[j]);
+    }
+}
+
 struct ItemInfo {
-    int e, row0, n, n_mma, mt;
+    int e, row0, n, n_mma, mt, z;
+    bool pool;
 };
 
 template <int MODE>
@@ -126,12 +157,14 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ int s_base[kMaxE + 1];     // first item of each active expert
     __shared__ int s_row0[kMaxE];
-    __shared__ int s_cnt[kMaxE];
+    __shared__ int s_cnt[kMaxE];          // routes of each expert, then of each active expert
+    __shared__ uint16_t s_blk[kMaxE];     // rows of its blocks
     __shared__ uint16_t s_act[kMaxE];
     __shared__ Items s_items;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+    __shared__ uint64_t a_full[kMaxStages], a_empty[kMaxStages], b_full[kMaxStages], b_empty[kMaxStages];
+    __shared__ uint64_t tfull[2], tempty[2];
     __shared__ __align__(16) float s_scale[kEpiWarps][kNMax];  // scales of the item's token rows, a copy per epilogue warp
 
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -141,8 +174,10 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(&full[i], 2);   // both producers
-            mbar_init(&empty[i], 1);
+            mbar_init(&a_full[i], MODE < kPhase1 ? 2 : 1);  // dense: both producers
+            mbar_init(&a_empty[i], 1);
+            mbar_init(&b_full[i], 1);
+            mbar_init(&b_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
@@ -183,6 +218,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                 const int pos = n_act + __popc(m & ((1u << lane) - 1u));
                 s_act[pos] = (uint16_t)e;
                 s_cnt[pos] = n;
+                s_blk[pos] = (uint16_t)block_rows(n);
                 s_row0[pos] = off;
                 s_base[pos] = run + inc - items;
             }
@@ -192,7 +228,9 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         rows = (int)__reduce_max_sync(kAll, (unsigned)rows);
         if (lane == 0) {
             s_base[n_act] = run;
-            s_items = Items{n_act, run, m_tiles, rows, min(kMaxStages, kRing / ((int)kABytes + rows * kKB))};
+            s_items.n_act = n_act;
+            s_items.total = run;
+            split_ring<MODE>(rows, &s_items);
         }
     }
     tc_fence_before();
@@ -201,25 +239,35 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
     // the next launch may take over SMs as this grid's CTAs finish
     pdl_launch_dependents();
     const uint32_t tmem = s_tmem;
-    const int total = s_items.total, n_act = s_items.n_act, S = s_items.stages;
-    const uint32_t stage_bytes = kABytes + (uint32_t)s_items.b_rows * kKB;
+    const int total = s_items.total, n_act = s_items.n_act;
+    const int SA = s_items.a_slots, SB = s_items.b_slots;
+    const uint32_t b_bytes = (uint32_t)s_items.b_rows * kKB;
+    uint8_t *ringb = ring + SA * kABytes;
+    // The dense product's rings go round together (both operands come from L2): one
+    // pair of barriers, so one wait and one commit a stage (5% at 4096x8192x2816)
+    uint64_t *bf = MODE < kPhase1 ? a_full : b_full, *be = MODE < kPhase1 ? a_empty : b_empty;
 
+    // Item -> (active expert, block of its routes, M tile), M tiles fastest.  A role
+    // takes its items in order, so the search goes on from the last one's expert.
+    int cur = 0;
     auto decode = [&](int item) {
-        int lo = 0, hi = n_act - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_base[mid] <= item) lo = mid; else hi = mid - 1;
-        }
-        const int rem = item - s_base[lo], nb = rem / m_tiles, n_e = s_cnt[lo], blk = block_rows(n_e);
+        while (cur + 1 < n_act && s_base[cur + 1] <= item) ++cur;
         ItemInfo r;
-        r.e = s_act[lo];
-        r.mt = rem - nb * m_tiles;
-        r.row0 = s_row0[lo] + nb * blk;
-        r.n = min(blk, n_e - nb * blk);
+        r.mt = item - s_base[cur];
+        const int blk = s_blk[cur];
+        int first = 0;
+        for (; r.mt >= m_tiles; r.mt -= m_tiles) first += blk;
+        r.e = s_act[cur];
+        r.row0 = s_row0[cur] + first;
+        r.n = min(blk, s_cnt[cur] - first);
         r.n_mma = (max(r.n, 1) + 15) & ~15;
+        r.z = 0;
+        r.pool = false;
         if (MODE >= kPhase1) {
             bool bad;
-            expert_slot(p.L, r.e, &bad);
+            const int slot = expert_slot(p.L, r.e, &bad);
+            r.pool = slot >= 0;
+            r.z = slot >= 0 ? slot : r.e;
             if (bad) record_error(0x2006u, (unsigned)__ldg(p.L.slot_table + r.e));
             if (r.row0 < 0 || r.n < 0 || r.row0 > p.R - r.n) {
                 record_error(0x2008u, (unsigned)item);
@@ -241,32 +289,25 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             // phases' launches follow this library's own (gather, codes of h),
             // which have waited for all before them and write no weights.
             if (MODE < kPhase1) pdl_wait();
-            const uint64_t pol = MODE < kPhase1 ? l2_policy_last() : l2_policy_first();
+            const uint64_t pol = MODE < kPhase1 ? l2_policy_normal() : l2_policy_first();
             int st = 0;
             uint32_t ph = 0;
             for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
                 const ItemInfo it = decode(item);
-                const CUtensorMap *ma = &map_home;
-                int z = 0;
-                if (MODE >= kPhase1) {
-                    bool bad;
-                    const int s = expert_slot(p.L, it.e, &bad);
-                    if (s >= 0) ma = &map_pool;
-                    z = s >= 0 ? s : it.e;
-                }
+                const CUtensorMap *ma = it.pool ? &map_pool : &map_home;
                 bool ok = true;
                 for (int kk = 0; kk < nk; ++kk) {
-                    if (!mbar_wait(&empty[st], ph ^ 1, &s_abort)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&full[st], kABytes);
-                    uint8_t *dst = ring + st * stage_bytes;
+                    if (!mbar_wait(&a_empty[st], ph ^ 1, &s_abort)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&a_full[st], kABytes);
+                    uint8_t *dst = ring + st * kABytes;
                     if (MODE == kPhase1) {
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
-                            tma_load_5d(dst + b * (kABytes / 4), ma, &full[st], kk * kKB, it.mt * 4 + b, z, pol);
+                            tma_load_5d(dst + b * (kABytes / 4), ma, &a_full[st], kk * kKB, it.mt * 4 + b, it.z, pol);
                     } else {
-                        tma_load_3d(dst, ma, &full[st], kk * kKB, it.mt * kM, z, pol);
+                        tma_load_3d(dst, ma, &a_full[st], kk * kKB, it.mt * kM, it.z, pol);
                     }
-                    if (++st == S) { st = 0; ph ^= 1; }
+                    if (++st == SA) { st = 0; ph ^= 1; }
                 }
                 if (!ok) break;
             }
@@ -275,7 +316,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         // -------------------------------------------------- tokens
         if (lane == 0) {
             pdl_wait();
-            const uint64_t pol = l2_policy_last();
+            const uint64_t pol = MODE < kPhase1 ? l2_policy_normal() : l2_policy_last();
             int st = 0;
             uint32_t ph = 0;
             for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
@@ -286,15 +327,15 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                 const int big = MODE < kPhase1 ? rows : 64;
                 bool ok = true;
                 for (int kk = 0; kk < nk; ++kk) {
-                    if (!mbar_wait(&empty[st], ph ^ 1, &s_abort)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&full[st], (uint32_t)rows * kKB);
-                    uint8_t *dst = ring + st * stage_bytes + kABytes;
+                    if (!mbar_wait(&be[st], ph ^ 1, &s_abort)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&bf[st], (uint32_t)rows * kKB);
+                    uint8_t *dst = ringb + st * b_bytes;
                     int j = 0;
                     for (; j + big <= rows; j += big)
-                        tma_load_2d(dst + j * kKB, &map_big, &full[st], kk * kKB, it.row0 + j, pol);
+                        tma_load_2d(dst + j * kKB, &map_big, &bf[st], kk * kKB, it.row0 + j, pol);
                     for (; j < rows; j += 16)
-                        tma_load_2d(dst + j * kKB, &map_b16, &full[st], kk * kKB, it.row0 + j, pol);
-                    if (++st == S) { st = 0; ph ^= 1; }
+                        tma_load_2d(dst + j * kKB, &map_b16, &bf[st], kk * kKB, it.row0 + j, pol);
+                    if (++st == SB) { st = 0; ph ^= 1; }
                 }
                 if (!ok) break;
             }
@@ -304,10 +345,10 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         // The whole warp walks the stages and an elected lane issues, so that the
         // descriptors stay in uniform registers.  A wait on a completed phase costs
         // ~130 cycles: the next stage's is tested before this one's products are issued.
-        int st = 0, acc = 0;
-        uint32_t ph = 0, aph = 0;
-        bool ready = false;
-        const uint64_t desc0 = sw128_desc(smem_u32(ring));
+        int sa = 0, sb = 0, acc = 0;
+        uint32_t pa = 0, pb = 0, aph = 0;
+        bool ra = false, rb = false;
+        const uint64_t desc_a = sw128_desc(smem_u32(ring)), desc_b = sw128_desc(smem_u32(ringb));
         for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
             const ItemInfo it = decode(item);
             if (!__all_sync(kAll, mbar_wait(&tempty[acc], aph ^ 1, &s_abort))) break;
@@ -318,12 +359,17 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                                    ((uint32_t)(kM >> 4) << 24);
             bool ok = true;
             for (int kk = 0; kk < nk; ++kk) {
-                if (!__all_sync(kAll, ready) && !__all_sync(kAll, mbar_wait(&full[st], ph, &s_abort))) { ok = false; break; }
+                if (!__all_sync(kAll, ra) && !__all_sync(kAll, mbar_wait(&a_full[sa], pa, &s_abort))) { ok = false; break; }
+                if (MODE >= kPhase1 && !__all_sync(kAll, rb) &&
+                    !__all_sync(kAll, mbar_wait(&b_full[sb], pb, &s_abort))) { ok = false; break; }
                 tc_fence_after();
-                const uint64_t ad = desc0 + (uint64_t)((st * stage_bytes) >> 4), bd = ad + (kABytes >> 4);
-                uint64_t *done = &empty[st];
-                if (++st == S) { st = 0; ph ^= 1; }
-                ready = mbar_test_wait(&full[st], ph);
+                const uint64_t ad = desc_a + (uint64_t)(sa * (kABytes >> 4));
+                const uint64_t bd = desc_b + (uint64_t)(sb * (b_bytes >> 4));
+                uint64_t *done_a = &a_empty[sa], *done_b = &b_empty[sb];
+                if (++sa == SA) { sa = 0; pa ^= 1; }
+                if (++sb == SB) { sb = 0; pb ^= 1; }
+                ra = mbar_test_wait(&a_full[sa], pa);
+                if (MODE >= kPhase1) rb = mbar_test_wait(&b_full[sb], pb);
                 // 32 codes of K per MMA: 32 bytes, 2 in the descriptor's address field.
                 // The four of a whole stage are unrolled: 128 cycles each at N = 256 (the
                 // tensor pipe's), where a counted loop took 144 to issue one
@@ -336,7 +382,8 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                     for (int j = 0; j < steps; ++j)
                         tc_mma_i8(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (kk | j) != 0);
                 }
-                tc_commit_warp(done);
+                tc_commit_warp(done_a);
+                if (MODE >= kPhase1) tc_commit_warp(done_b);
             }
             if (!ok) break;
             tc_commit_warp(&tfull[acc]);
@@ -350,6 +397,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         const int half = lane >> 4;
         int acc = 0;
         uint32_t aph = 0;
+        const uint64_t h_pol = l2_policy_last();  // the next launch reads h
         pdl_wait();  // the token rows' scales come from the launch before
         for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
             const ItemInfo it = decode(item);
@@ -388,9 +436,14 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                         v[j] = gate_up(half ? oth : own, half ? own : oth, half ? s2.y : s2.x, sw, su);
                     }
                     float *o = static_cast<float *>(p.out) + (size_t)(it.row0 + c0 + half) * p.M + m;
+                    if (c0 + 32 <= it.n) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c0 + half + 2 * j < it.n) o[(size_t)(2 * j) * p.M] = v[j];
+                        for (int j = 0; j < 16; ++j) st_f32_hint(o + (size_t)(2 * j) * p.M, v[j], h_pol);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (c0 + half + 2 * j < it.n) st_f32_hint(o + (size_t)(2 * j) * p.M, v[j], h_pol);
+                    }
                 } else {
                     float v[32];
 #pragma unroll
@@ -402,17 +455,9 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                         v[j + 3] = scaled(raw[j + 3], s4.w, sw);
                     }
                     const size_t at = (size_t)(it.row0 + c0) * p.M + m;
-                    if (MODE == kLinear) {
-                        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + at;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (c0 + j < it.n && m < p.M) o[(size_t)j * p.M] = __float2bfloat16_rn(v[j]);
-                    } else {
-                        float *o = static_cast<float *>(p.out) + at;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (c0 + j < it.n && m < p.M) o[(size_t)j * p.M] = v[j];
-                    }
+                    if (m >= p.M) continue;  // a row past the matrix
+                    if (MODE == kLinear) store_cols(static_cast<__nv_bfloat16 *>(p.out) + at, p.M, v, it.n - c0);
+                    else store_cols(static_cast<float *>(p.out) + at, p.M, v, it.n - c0);
                 }
             }
             tc_fence_before();
@@ -468,36 +513,45 @@ __global__ void __launch_bounds__(256) k_gather_i8(const int8_t *__restrict__ xq
     }
 }
 
-// Codes and scale of each row of h, one warp per row.
+// Codes and scale of each row of h, one warp per row; V > 0: rows of at most 128 V
+// values, held in registers; V = 0: read twice.
+template <int V>
 __global__ void __launch_bounds__(256) k_codes_h(const float *__restrict__ h, const int32_t *__restrict__ offsets, int E,
                                                  int I, int R, int8_t *__restrict__ hq, float *__restrict__ sh) {
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, n = min(__ldg(offsets + E), R);
-    const int warps = (int)(gridDim.x * (blockDim.x >> 5));
-    for (int s = (int)(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)); s < n; s += warps) {
-        const float4 *src = reinterpret_cast<const float4 *>(h + (size_t)s * I);
-        float amax = 0.0f;
-        for (int c = lane; c < I / 4; c += 32) {
-            const float4 v = src[c];
-            amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-        }
+    const int lane = threadIdx.x & 31, n = min(__ldg(offsets + E), R), per = I / 4;
+    const int s = (int)(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5));
+    if (s >= n) return;
+    const float4 *src = reinterpret_cast<const float4 *>(h + (size_t)s * I);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(hq + (size_t)s * I);
+    float4 v[V > 0 ? V : 1];
+    float amax = 0.0f;
+    auto grow = [&](float4 u) { amax = fmaxf(amax, fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w)))); };
+    if (V > 0) {
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
-        const float sc = __fdiv_rn(amax, 127.0f);
-        for (int c = lane; c < I / 4; c += 32) {
-            const float4 v = src[c];
-            reinterpret_cast<uint32_t *>(hq + (size_t)s * I)[c] =
-                ((uint32_t)code_i8(v.x, sc) & 0xffu) | (((uint32_t)code_i8(v.y, sc) & 0xffu) << 8) |
-                (((uint32_t)code_i8(v.z, sc) & 0xffu) << 16) | (((uint32_t)code_i8(v.w, sc) & 0xffu) << 24);
-        }
-        if (lane == 0) sh[s] = sc;
+        for (int i = 0; i < V; ++i)
+            v[i] = lane + 32 * i < per ? src[lane + 32 * i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) grow(v[i]);
+    } else {
+        for (int c = lane; c < per; c += 32) grow(src[c]);
     }
+    amax = warp_max(amax);
+    const CodeScale sc = code_scale(amax);
+    if (V > 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane + 32 * i < per) dst[lane + 32 * i] = sc.code4(v[i]);
+    } else {
+        for (int c = lane; c < per; c += 32) dst[c] = sc.code4(src[c]);
+    }
+    if (lane == 0) sh[s] = sc.s;
 }
 
 // ------------------------------------------------------------------ host side
 constexpr size_t kDynSmem = 1024 + kRing;
-static_assert(kDynSmem + 4 * (3 * kMaxE + 1) + 2 * kMaxE + 4 * kEpiWarps * kNMax + 512 <= 232448, "int8 tensor-core kernel exceeds shared memory");
+static_assert(kDynSmem + 4 * (3 * kMaxE + 1) + 4 * kMaxE + 4 * kEpiWarps * kNMax + 768 <= 232448, "int8 tensor-core kernel exceeds shared memory");
 
 // W13 codes of every blob: {K, 16 rows, blocks of 16 rows, gate or up, blob},
 // box = 16 gate rows and their 16 up rows.
@@ -608,7 +662,9 @@ cudaError_t launch_ffn_i8_tc(const FfnI8Args &a, cudaStream_t s) {
     p.brow = ss;
     p.out = h;
     if ((err = launch_tc<kPhase1>(h1, p1, xs, p, n_sm, s)) != cudaSuccess) return err;
-    err = launch_pdl(k_codes_h, dim3((unsigned)blocks), dim3(256), 0, s, (const float *)h, a.offsets, E, I, R, hq, sh);
+    const dim3 rows8((unsigned)((R + 7) / 8));
+    if (I <= 768) err = launch_pdl(k_codes_h<6>, rows8, dim3(256), 0, s, (const float *)h, a.offsets, E, I, R, hq, sh);
+    else err = launch_pdl(k_codes_h<0>, rows8, dim3(256), 0, s, (const float *)h, a.offsets, E, I, R, hq, sh);
     if (err != cudaSuccess) return err;
     p.K = I;
     p.M = H;

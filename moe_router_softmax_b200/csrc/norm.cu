@@ -8,6 +8,7 @@
 //   y  = residual_scale * residual + block_scale * gate_t[t] * gate_h[h] * zn
 //   xn = y * rsqrt(mean(y^2) + eps) * (offset + next_w)             (y as stored)
 //   sx = max |xn| / 127,  xq = rint(xn / sx)                        (xn before its rounding)
+#include "i8_math.cuh"
 #include "ops.cuh"
 
 namespace moe {
@@ -133,18 +134,15 @@ __global__ void __launch_bounds__(1024) k_norm(const NormArgs a) {
         if (a.xn) reinterpret_cast<uint4 *>(a.xn + base)[ch] = pack8(v[c]);
     }
     if (a.xq == nullptr) return;
-    const float s = block_reduce<true>(amax, s_part) / 127.0f;
-    if (threadIdx.x == 0) a.sx[t] = s;
+    const CodeScale sc = code_scale(block_reduce<true>(amax, s_part));
+    if (threadIdx.x == 0) a.sx[t] = sc.s;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int ch = threadIdx.x + c * blockDim.x;
         if (ch >= nch) continue;
-        uint32_t o[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            o[i >> 2] |= ((uint32_t)code_i8(v[c][i], s) & 0xffu) << (8 * (i & 3));
-        }
-        reinterpret_cast<uint2 *>(a.xq + base)[ch] = make_uint2(o[0], o[1]);
+        reinterpret_cast<uint2 *>(a.xq + base)[ch] =
+            make_uint2(sc.code4(make_float4(v[c][0], v[c][1], v[c][2], v[c][3])),
+                       sc.code4(make_float4(v[c][4], v[c][5], v[c][6], v[c][7])));
     }
 }
 

@@ -64,21 +64,4 @@ cudaError_t launch_ffn_i8_tc(const FfnI8Args &a, cudaStream_t s);
 cudaError_t i8_take_error(unsigned *code, unsigned *info);
 cudaError_t i8tc_take_error(unsigned *code, unsigned *info);
 
-// The scales' products and the gate, in a fixed order of roundings: every kernel
-// that takes a shape gives the same bits.
-__device__ __forceinline__ float scaled(int sum, float s_token, float s_row) {
-    return __fmul_rn(__fmul_rn((float)sum, s_token), s_row);
-}
-__device__ __forceinline__ float gate_up(int g_sum, int u_sum, float s_token, float s_gate, float s_up) {
-    const float v = scaled(g_sum, s_token, s_gate), u = scaled(u_sum, s_token, s_up);
-    const float cube = __fmul_rn(__fmul_rn(v, v), v);
-    const float t = tanhf(__fmul_rn(0.7978845608028654f, __fmaf_rn(0.044715f, cube, v)));  // sqrt(2/pi)
-    return __fmul_rn(__fmul_rn(__fmul_rn(0.5f, v), __fadd_rn(1.0f, t)), u);
-}
-
-// int8 code of v at scale s (moe_quantize_int8's steps); 0 at s = 0 and for a NaN.
-__device__ __forceinline__ int code_i8(float v, float s) {
-    return s != 0.0f ? max(-127, min(127, (int)rintf(__fdiv_rn(v, s)))) : 0;
-}
-
 }  // namespace moe

@@ -97,6 +97,11 @@ __device__ __forceinline__ uint64_t l2_policy_last() {
     asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
+__device__ __forceinline__ uint64_t l2_policy_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
 // Stores of the intermediates a later launch re-reads (xs by every M tile of
 // phase 1, h by every M tile of phase 2) with the evict-last policy, so they
 // stay in L2 beside the evict-first weight stream instead of going to DRAM
@@ -108,6 +113,9 @@ __device__ __forceinline__ void st_v4_hint(void *dst, uint4 u, uint64_t pol) {
 }
 __device__ __forceinline__ void st_u16_hint(uint16_t *dst, uint16_t v, uint64_t pol) {
     asm volatile("st.global.L2::cache_hint.u16 [%0], %1, %2;" ::"l"(dst), "h"(v), "l"(pol) : "memory");
+}
+__device__ __forceinline__ void st_f32_hint(float *dst, float v, uint64_t pol) {
+    asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(dst), "f"(v), "l"(pol) : "memory");
 }
 __device__ __forceinline__ void tma_load_2d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int x, int y,
                                             uint64_t pol) {
