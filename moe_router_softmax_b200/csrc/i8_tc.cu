@@ -20,9 +20,9 @@
 // Persistent CTAs, one per SM; warp 0 TMA producer of the weights, warp 1 TMEM
 // allocation and the MMA issuer, warps 2..9 epilogue (TMEM -> registers ->
 // global; warp w reads lanes 32 (w % 4) ..), warp 10 TMA producer of the tokens.
-// Two rings of stages of 128 codes of K, one of weight tiles and one of token blocks,
-// whose slots share the CTA's memory by the launch's largest block: the weights come
-// from HBM and want many stages in flight, the tokens from L2.  Two accumulators of
+// Two rings of stages of K, one of weight tiles and one of token blocks, whose slots
+// share the CTA's memory by the launch's largest block: the weights come from HBM and
+// want many bytes in flight, the tokens from L2.  Two accumulators of
 // 256 columns, so that an item's epilogue overlaps the next item's products.  Every
 // wait is bounded: on a timeout the kernel records it and every role drains out.
 #include <cuda_bf16.h>
@@ -40,9 +40,9 @@ using namespace tc;
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kM = 128;                        // weight rows per tile
-constexpr int kKB = 128;                       // codes of K per stage: one swizzle row
+constexpr int kKB = 128;                       // codes of K per swizzle row (an atom of a stage)
 constexpr int kNMax = 256;                     // tokens per block
-constexpr uint32_t kABytes = kM * kKB;         // 16 KB
+constexpr uint32_t kABytes = kM * kKB;         // 16 KB: an atom of a weight stage
 constexpr int kRing = 198 * 1024;
 constexpr int kMaxStages = 12;                 // of either ring
 constexpr int kEpiWarps = 8;                   // two per TMEM quadrant
@@ -109,17 +109,21 @@ struct Items {
     int n_act, total, b_rows, a_slots, b_slots;
 };
 
-// Slots of the two rings for token blocks of `rows` rows.  The dense product's
-// operands both come from L2 and get the same number.  So do the phases' up to 64
-// rows; above, three token slots leave the rest of the memory to the weights.
-template <int MODE>
+// Slots of the two rings for token blocks of `rows` rows and stages of ATOMS atoms
+// of K.  Every role pays a few hundred cycles of waits and commits a stage, while an
+// SM's share of HBM brings a weight atom in ~700 cycles.  So the phases take two atoms
+// at a time where experts hold few routes (FFN of 64 tokens 120 -> 116 us); with many,
+// the weights in flight count for more than the waits (2047 tokens: two atoms 315 us,
+// one 296), and three token slots leave them the rest of the memory.  The dense
+// product's operands both come from L2 and get the same number of slots.
+template <int MODE, int ATOMS>
 __device__ __forceinline__ void split_ring(int rows, Items *it) {
-    const int b = rows * kKB;
-    const int even = min(kMaxStages, kRing / ((int)kABytes + b));
+    const int a = ATOMS * (int)kABytes, b = ATOMS * rows * kKB, even = min(kMaxStages, kRing / (a + b));
     it->b_rows = rows;
-    it->b_slots = MODE < kPhase1 || rows <= 64 ? even : 3;
-    it->a_slots = MODE < kPhase1 ? even : min(kMaxStages, (kRing - it->b_slots * b) / (int)kABytes);
+    it->b_slots = MODE < kPhase1 || rows <= 64 ? even : 4 - ATOMS;
+    it->a_slots = MODE < kPhase1 ? even : min(kMaxStages, (kRing - it->b_slots * b) / a);
 }
+constexpr int kFewRoutes = 32;  // two atoms a stage up to so many routes per expert on average
 
 // Blocks of an expert's n routes: as few as kNMax allows, of even size, a
 // multiple of 16 (the MMA's N).
@@ -150,10 +154,15 @@ struct ItemInfo {
     bool pool;
 };
 
-template <int MODE>
+// Boxes of the token rows: dense, the block of the launch; phases, 16 << i rows.
+struct TokenMaps {
+    CUtensorMap m[4];
+};
+
+template <int MODE, int ATOMS>
 __global__ void __launch_bounds__(kThreads, 1)
 k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CUtensorMap map_pool,
-        const __grid_constant__ CUtensorMap map_b16, const __grid_constant__ CUtensorMap map_big, const TcI8Params p) {
+        const __grid_constant__ TokenMaps map_b, const TcI8Params p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ int s_base[kMaxE + 1];     // first item of each active expert
     __shared__ int s_row0[kMaxE];
@@ -170,7 +179,6 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m_tiles = MODE == kPhase1 ? p.M / 64 : (p.M + kM - 1) / kM;
-    const int nk = (p.K + kKB - 1) / kKB;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -230,7 +238,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             s_base[n_act] = run;
             s_items.n_act = n_act;
             s_items.total = run;
-            split_ring<MODE>(rows, &s_items);
+            split_ring<MODE, ATOMS>(rows, &s_items);
         }
     }
     tc_fence_before();
@@ -241,8 +249,10 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
     const uint32_t tmem = s_tmem;
     const int total = s_items.total, n_act = s_items.n_act;
     const int SA = s_items.a_slots, SB = s_items.b_slots;
-    const uint32_t b_bytes = (uint32_t)s_items.b_rows * kKB;
-    uint8_t *ringb = ring + SA * kABytes;
+    const int n_atoms = (p.K + kKB - 1) / kKB, nk = (n_atoms + ATOMS - 1) / ATOMS;
+    auto atoms_at = [&](int kk) { return min(ATOMS, n_atoms - kk * ATOMS); };
+    const uint32_t b_atom = (uint32_t)s_items.b_rows * kKB, b_bytes = ATOMS * b_atom, a_bytes = ATOMS * kABytes;
+    uint8_t *ringb = ring + SA * a_bytes;
     // The dense product's rings go round together (both operands come from L2): one
     // pair of barriers, so one wait and one commit a stage (5% at 4096x8192x2816)
     uint64_t *bf = MODE < kPhase1 ? a_full : b_full, *be = MODE < kPhase1 ? a_empty : b_empty;
@@ -298,14 +308,18 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                 bool ok = true;
                 for (int kk = 0; kk < nk; ++kk) {
                     if (!mbar_wait(&a_empty[st], ph ^ 1, &s_abort)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&a_full[st], kABytes);
-                    uint8_t *dst = ring + st * kABytes;
-                    if (MODE == kPhase1) {
+                    const int na = atoms_at(kk);
+                    mbar_arrive_expect_tx(&a_full[st], na * kABytes);
+                    for (int a = 0; a < na; ++a) {
+                        uint8_t *dst = ring + st * a_bytes + a * kABytes;
+                        const int x = (kk * ATOMS + a) * kKB;
+                        if (MODE == kPhase1) {
 #pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            tma_load_5d(dst + b * (kABytes / 4), ma, &a_full[st], kk * kKB, it.mt * 4 + b, it.z, pol);
-                    } else {
-                        tma_load_3d(dst, ma, &a_full[st], kk * kKB, it.mt * kM, it.z, pol);
+                            for (int b = 0; b < 4; ++b)
+                                tma_load_5d(dst + b * (kABytes / 4), ma, &a_full[st], x, it.mt * 4 + b, it.z, pol);
+                        } else {
+                            tma_load_3d(dst, ma, &a_full[st], x, it.mt * kM, it.z, pol);
+                        }
                     }
                     if (++st == SA) { st = 0; ph ^= 1; }
                 }
@@ -322,19 +336,30 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
                 const ItemInfo it = decode(item);
                 // dense: the whole block in one box (rows past the last token read as
-                // zeros); phases: boxes of 64 rows, then of 16
+                // zeros); phases: boxes of 128, 64, 32 and 16 rows
                 const int rows = MODE < kPhase1 ? s_items.b_rows : it.n_mma;
-                const int big = MODE < kPhase1 ? rows : 64;
                 bool ok = true;
                 for (int kk = 0; kk < nk; ++kk) {
                     if (!mbar_wait(&be[st], ph ^ 1, &s_abort)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&bf[st], (uint32_t)rows * kKB);
-                    uint8_t *dst = ringb + st * b_bytes;
-                    int j = 0;
-                    for (; j + big <= rows; j += big)
-                        tma_load_2d(dst + j * kKB, &map_big, &bf[st], kk * kKB, it.row0 + j, pol);
-                    for (; j < rows; j += 16)
-                        tma_load_2d(dst + j * kKB, &map_b16, &bf[st], kk * kKB, it.row0 + j, pol);
+                    const int na = atoms_at(kk);
+                    mbar_arrive_expect_tx(&bf[st], (uint32_t)(na * rows * kKB));
+                    for (int a = 0; a < na; ++a) {
+                        uint8_t *dst = ringb + st * b_bytes + a * b_atom;
+                        const int x = (kk * ATOMS + a) * kKB;
+                        if (MODE < kPhase1) {
+                            tma_load_2d(dst, &map_b.m[0], &bf[st], x, it.row0, pol);
+                        } else {
+                            int j = 0;
+                            for (; j + 128 <= rows; j += 128)
+                                tma_load_2d(dst + j * kKB, &map_b.m[3], &bf[st], x, it.row0 + j, pol);
+#pragma unroll
+                            for (int i = 2; i >= 0; --i)
+                                if (rows & (16 << i)) {
+                                    tma_load_2d(dst + j * kKB, &map_b.m[i], &bf[st], x, it.row0 + j, pol);
+                                    j += 16 << i;
+                                }
+                        }
+                    }
                     if (++st == SB) { st = 0; ph ^= 1; }
                 }
                 if (!ok) break;
@@ -363,7 +388,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                 if (MODE >= kPhase1 && !__all_sync(kAll, rb) &&
                     !__all_sync(kAll, mbar_wait(&b_full[sb], pb, &s_abort))) { ok = false; break; }
                 tc_fence_after();
-                const uint64_t ad = desc_a + (uint64_t)(sa * (kABytes >> 4));
+                const uint64_t ad = desc_a + (uint64_t)(sa * (a_bytes >> 4));
                 const uint64_t bd = desc_b + (uint64_t)(sb * (b_bytes >> 4));
                 uint64_t *done_a = &a_empty[sa], *done_b = &b_empty[sb];
                 if (++sa == SA) { sa = 0; pa ^= 1; }
@@ -371,16 +396,21 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                 ra = mbar_test_wait(&a_full[sa], pa);
                 if (MODE >= kPhase1) rb = mbar_test_wait(&b_full[sb], pb);
                 // 32 codes of K per MMA: 32 bytes, 2 in the descriptor's address field.
-                // The four of a whole stage are unrolled: 128 cycles each at N = 256 (the
+                // The four of a whole atom are unrolled: 128 cycles each at N = 256 (the
                 // tensor pipe's), where a counted loop took 144 to issue one
-                if ((kk + 1) * kKB <= p.K) {
+                const int na = atoms_at(kk);
+                for (int a = 0; a < na; ++a) {
+                    const uint64_t ada = ad + (uint64_t)(a * (kABytes >> 4)), bda = bd + (uint64_t)(a * (b_atom >> 4));
+                    const int left = p.K - (kk * ATOMS + a) * kKB;
+                    if (left >= kKB) {
 #pragma unroll
-                    for (int j = 0; j < kKB / 32; ++j)
-                        tc_mma_i8(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (kk | j) != 0);
-                } else {
-                    const int steps = (p.K - kk * kKB + 31) / 32;  // past K both operands hold zeros
-                    for (int j = 0; j < steps; ++j)
-                        tc_mma_i8(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), idesc, (kk | j) != 0);
+                        for (int j = 0; j < kKB / 32; ++j)
+                            tc_mma_i8(d, ada + (uint64_t)(2 * j), bda + (uint64_t)(2 * j), idesc, (kk | a | j) != 0);
+                    } else {
+                        const int steps = (left + 31) / 32;  // past K both operands hold zeros
+                        for (int j = 0; j < steps; ++j)
+                            tc_mma_i8(d, ada + (uint64_t)(2 * j), bda + (uint64_t)(2 * j), idesc, (kk | a | j) != 0);
+                    }
                 }
                 tc_commit_warp(done_a);
                 if (MODE >= kPhase1) tc_commit_warp(done_b);
@@ -565,18 +595,15 @@ bool encode_w13(CUtensorMap *m, const void *base, uint64_t H, uint64_t I, uint64
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE>
+template <int MODE, int ATOMS>
 cudaError_t launch_tc(const CUtensorMap &mh, const CUtensorMap &mp, const void *b, const TcI8Params &p, int n_sm,
                       cudaStream_t s) {
-    CUtensorMap b16, big;
-    // dense: the block that the kernel will take; phases: 64 rows
-    const int big_rows = MODE < kPhase1 ? block_rows(p.R) : 64;
-    if (!encode_2d(&b16, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)p.K, (uint64_t)p.R, kKB, 16,
-                   CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_2d(&big, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)p.K, (uint64_t)p.R, kKB, (uint32_t)big_rows,
-                   CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
-    auto kern = k_i8_tc<MODE>;
+    TokenMaps mb;
+    for (int i = 0; i < 4; ++i)
+        if (!encode_2d(&mb.m[i], b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)p.K, (uint64_t)p.R, kKB,
+                       MODE < kPhase1 ? (uint32_t)block_rows(p.R) : 16u << i, CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    auto kern = k_i8_tc<MODE, ATOMS>;
     static bool attr[kMaxDevices] = {};
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -587,7 +614,7 @@ cudaError_t launch_tc(const CUtensorMap &mh, const CUtensorMap &mp, const void *
         if (err != cudaSuccess) return err;
         attr[dev] = true;
     }
-    return launch_pdl(kern, dim3((unsigned)n_sm), dim3(kThreads), kDynSmem, s, mh, mp, b16, big, p);
+    return launch_pdl(kern, dim3((unsigned)n_sm), dim3(kThreads), kDynSmem, s, mh, mp, mb, p);
 }
 
 size_t a256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -610,7 +637,7 @@ cudaError_t launch_linear_i8_tc(const LinearArgs &a, cudaStream_t s) {
     p.brow = a.sx;
     p.wscale = a.sw;
     p.out = a.y;
-    return a.fp32 ? launch_tc<kLinearF32>(mw, mw, a.xq, p, n_sm, s) : launch_tc<kLinear>(mw, mw, a.xq, p, n_sm, s);
+    return a.fp32 ? launch_tc<kLinearF32, 1>(mw, mw, a.xq, p, n_sm, s) : launch_tc<kLinear, 1>(mw, mw, a.xq, p, n_sm, s);
 }
 
 // h fp32 | codes of h | scales of h | gathered codes | gathered scales
@@ -661,7 +688,9 @@ cudaError_t launch_ffn_i8_tc(const FfnI8Args &a, cudaStream_t s) {
     p.M = I;
     p.brow = ss;
     p.out = h;
-    if ((err = launch_tc<kPhase1>(h1, p1, xs, p, n_sm, s)) != cudaSuccess) return err;
+    const bool few = (int64_t)R <= (int64_t)E * kFewRoutes;
+    err = few ? launch_tc<kPhase1, 2>(h1, p1, xs, p, n_sm, s) : launch_tc<kPhase1, 1>(h1, p1, xs, p, n_sm, s);
+    if (err != cudaSuccess) return err;
     const dim3 rows8((unsigned)((R + 7) / 8));
     if (I <= 768) err = launch_pdl(k_codes_h<6>, rows8, dim3(256), 0, s, (const float *)h, a.offsets, E, I, R, hq, sh);
     else err = launch_pdl(k_codes_h<0>, rows8, dim3(256), 0, s, (const float *)h, a.offsets, E, I, R, hq, sh);
@@ -670,7 +699,7 @@ cudaError_t launch_ffn_i8_tc(const FfnI8Args &a, cudaStream_t s) {
     p.M = H;
     p.brow = sh;
     p.out = a.rows;
-    return launch_tc<kPhase2>(h2, p2, hq, p, n_sm, s);
+    return few ? launch_tc<kPhase2, 2>(h2, p2, hq, p, n_sm, s) : launch_tc<kPhase2, 1>(h2, p2, hq, p, n_sm, s);
 }
 
 cudaError_t i8tc_take_error(unsigned *code, unsigned *info) {
