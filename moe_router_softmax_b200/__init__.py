@@ -118,9 +118,9 @@ def _check(st: int) -> None:
 
 
 def _stream(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    # the current stream's raw handle: building a Stream object for it costs 3 us
+    raw = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+    return ctypes.c_void_p(raw)
 
 
 def _dev(t: torch.Tensor | None, dtype=None, name="tensor"):
@@ -528,12 +528,12 @@ def moe_ep_splits(counts: np.ndarray, recv_counts: np.ndarray):
 # Their arguments are checked against one another as well (shapes, one device),
 # and a call runs on its tensors' device whatever the current one is.
 
-def _arg(t, shape, dtype, name: str, dev):
-    """Device address of a tensor argument, or None for None."""
+def _arg(t, shape, dtype, name: str, dev: int):
+    """Device address of a tensor argument on CUDA device `dev`, or None for None."""
     if t is None:
         return None
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
@@ -543,23 +543,21 @@ def _arg(t, shape, dtype, name: str, dev):
     return t.data_ptr()
 
 
-def _device_of(t: torch.Tensor, ndim: int, name: str):
+def _device_of(t: torch.Tensor, ndim: int, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions")
-    return t.device
+    return t.get_device()
 
 
-def _call(fn, dev, stream, *args) -> None:
-    """Run an entry point on `dev`, on `stream` or the device's current stream."""
-    idx = dev.index
-    # the stream's raw handle: building a Stream object would cost a third of a small call
-    raw = torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream
-    if idx == torch.cuda.current_device():
+def _call(fn, dev: int, stream, *args) -> None:
+    """Run an entry point on device `dev`, on `stream` or the device's current stream."""
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
         st = fn(*args, raw)
     else:
-        with torch.cuda.device(idx):
+        with torch.cuda.device(dev):
             st = fn(*args, raw)
     if st != MOE_OK:
         _check(st)
@@ -608,13 +606,13 @@ def moe_grouped_ffn_w8a8(layer: MoeLayer, xq: torch.Tensor, sx: torch.Tensor, k:
     scales sx [T], as moe_norm or moe_quantize_int8 make them): fp32 rows
     [T*k, H] in sorted order, for moe_combine or moe_combine_norm."""
     dev = _device_of(xq, 2, "xq")
-    if layer.home.device != dev:
-        raise ValueError(f"the layer is on {layer.home.device}, xq on {dev}")
+    if layer.home.get_device() != dev:
+        raise ValueError(f"the layer is on {layer.home.device}, xq on {xq.device}")
     T, R = xq.shape[0], xq.shape[0] * k
     if rows is None:
-        rows = torch.empty((R, layer.H), dtype=torch.float32, device=dev)
+        rows = xq.new_empty((R, layer.H), dtype=torch.float32)
     if ws is None:
-        ws = torch.empty(max(moe_grouped_ffn_w8a8_workspace(layer, T, k), 16), dtype=torch.uint8, device=dev)
+        ws = xq.new_empty(max(moe_grouped_ffn_w8a8_workspace(layer, T, k), 16), dtype=torch.uint8)
     _call(_lib.moe_grouped_ffn_w8a8, dev, stream, layer.ref(), _arg(xq, (T, layer.H), torch.int8, "xq", dev),
           _arg(sx, (T,), torch.float32, "sx", dev), T, k, _arg(counts, (layer.E,), torch.int32, "counts", dev),
           _arg(offsets, (layer.E + 1,), torch.int32, "offsets", dev),
@@ -631,11 +629,11 @@ class NormOut(NamedTuple):
     sx: Optional[torch.Tensor]  # fp32 [T], their scales
 
 
-def _norm_out(like, T, H, y, xn, xq, sx, want_xn, codes) -> NormOut:
+def _norm_out(like, T, y, xn, xq, sx, want_xn, codes) -> NormOut:
     if xn is None and want_xn:
-        xn = like.new_empty((T, H), dtype=torch.bfloat16)
+        xn = torch.empty_like(like)
     if codes:
-        xq = like.new_empty((T, H), dtype=torch.int8) if xq is None else xq
+        xq = torch.empty_like(like, dtype=torch.int8) if xq is None else xq
         sx = like.new_empty((T,), dtype=torch.float32) if sx is None else sx
     return NormOut(y, xn, xq, sx)
 
@@ -647,7 +645,7 @@ def moe_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: f
     (``want_xn``) and, with ``codes``, as int8 codes with a scale per token."""
     dev = _device_of(x, 2, "x")
     T, H = x.shape
-    o = _norm_out(x, T, H, None, xn, xq, sx, want_xn, codes)
+    o = _norm_out(x, T, None, xn, xq, sx, want_xn, codes)
     bf = torch.bfloat16
     _call(_lib.moe_norm, dev, stream, _arg(x, (T, H), bf, "x", dev), _arg(weight, (H,), bf, "weight", dev), T, H, eps,
           offset, _arg(o.xn, (T, H), bf, "xn", dev), _arg(o.xq, (T, H), torch.int8, "xq", dev),
@@ -655,15 +653,12 @@ def moe_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: f
     return o
 
 
-def _after_block(fn, src, residual, post_weight, gate_h, gate_t, next_weight, eps, offset, residual_scale, block_scale,
-                 codes, want_xn, y, xn, xq, sx, stream) -> NormOut:
-    dev = _device_of(residual, 2, "residual")
-    T, H = residual.shape
+def _after_block(fn, dev, src, T, H, residual, post_weight, gate_h, gate_t, next_weight, eps, offset, residual_scale,
+                 block_scale, codes, want_xn, y, xn, xq, sx, stream) -> NormOut:
     bf, fp = torch.bfloat16, torch.float32
-    y = residual.new_empty((T, H), dtype=bf) if y is None else y
-    has_next = next_weight is not None
-    o = _norm_out(residual, T, H, y, xn, xq, sx, want_xn and has_next, codes)
-    _call(fn, dev, stream, *src(T, H, dev), _arg(residual, (T, H), bf, "residual", dev),
+    y = torch.empty_like(residual) if y is None else y
+    o = _norm_out(residual, T, y, xn, xq, sx, want_xn and next_weight is not None, codes)
+    _call(fn, dev, stream, *src, _arg(residual, (T, H), bf, "residual", dev),
           _arg(post_weight, (H,), bf, "post_weight", dev), _arg(gate_h, (H,), fp, "gate_h", dev),
           _arg(gate_t, (T,), fp, "gate_t", dev), _arg(next_weight, (H,), bf, "next_weight", dev), T, H, eps, offset,
           residual_scale, block_scale, _arg(y, (T, H), bf, "y", dev), _arg(o.xn, (T, H), bf, "xn", dev),
@@ -679,12 +674,12 @@ def moe_residual_norm(z: torch.Tensor, residual: torch.Tensor, post_weight: torc
                       sx: torch.Tensor | None = None, stream=None) -> NormOut:
     """After a dense block: y = residual_scale * residual + block_scale * gate_t *
     gate_h * norm(z), and y normalised for the next block (``next_weight``) as bf16
-    and, with ``codes``, as int8 codes."""
-    def src(T, H, dev):
-        return (_arg(z, (T, H), torch.bfloat16, "z", dev),)
-
-    return _after_block(_lib.moe_residual_norm, src, residual, post_weight, gate_h, gate_t, next_weight, eps, offset,
-                        residual_scale, block_scale, codes, want_xn, y, xn, xq, sx, stream)
+    and, with ``codes``, as int8 codes.  ``y`` may be ``residual`` or ``z``."""
+    dev = _device_of(residual, 2, "residual")
+    T, H = residual.shape
+    src = (_arg(z, (T, H), torch.bfloat16, "z", dev),)
+    return _after_block(_lib.moe_residual_norm, dev, src, T, H, residual, post_weight, gate_h, gate_t, next_weight, eps,
+                        offset, residual_scale, block_scale, codes, want_xn, y, xn, xq, sx, stream)
 
 
 def moe_combine_norm(rows: torch.Tensor, route_pos: torch.Tensor, w: torch.Tensor, residual: torch.Tensor,
@@ -695,16 +690,15 @@ def moe_combine_norm(rows: torch.Tensor, route_pos: torch.Tensor, w: torch.Tenso
                      xq: torch.Tensor | None = None, sx: torch.Tensor | None = None, stream=None) -> NormOut:
     """After the experts: moe_residual_norm of the combined rows (moe_combine's sum,
     kept in fp32); rows fp32 [T*k, H], route_pos int32 [T*k], w fp32 [T, k]."""
+    dev = _device_of(residual, 2, "residual")
+    T, H = residual.shape
     if w.dim() != 2:
         raise ValueError("w must have 2 dimensions")
     k = w.shape[1]
-
-    def src(T, H, dev):
-        return (_arg(rows, (T * k, H), torch.float32, "rows", dev),
-                _arg(route_pos, (T * k,), torch.int32, "route_pos", dev), _arg(w, (T, k), torch.float32, "w", dev), k)
-
-    return _after_block(_lib.moe_combine_norm, src, residual, post_weight, gate_h, gate_t, next_weight, eps, offset,
-                        residual_scale, block_scale, codes, want_xn, y, xn, xq, sx, stream)
+    src = (_arg(rows, (T * k, H), torch.float32, "rows", dev), _arg(route_pos, (T * k,), torch.int32, "route_pos", dev),
+           _arg(w, (T, k), torch.float32, "w", dev), k)
+    return _after_block(_lib.moe_combine_norm, dev, src, T, H, residual, post_weight, gate_h, gate_t, next_weight, eps,
+                        offset, residual_scale, block_scale, codes, want_xn, y, xn, xq, sx, stream)
 
 
 # ------------------------------------------------------------------ helpers

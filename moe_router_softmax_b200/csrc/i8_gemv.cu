@@ -80,82 +80,111 @@ __device__ __forceinline__ int expert_of_row(const int32_t *offsets, int E, int 
     return __reduce_add_sync(kAll, n);
 }
 
-// Phase 1: one warp per sorted row and intermediate column (a gate row and its
-// up row of W13).
-__global__ void __launch_bounds__(32 * kWarps) k_ffn_i8_gemv1(const FfnI8Args a, float *__restrict__ h) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, I = a.L.I, H = a.L.H, per = I / kWarps;
-    const int s = blockIdx.x / per, i = (blockIdx.x % per) * kWarps + (threadIdx.x >> 5);
-    const int R = a.T * a.k;
-    if (s >= min(__ldg(a.offsets + a.L.E), R)) return;
+// Blob of the expert that sorted row s belongs to, or null where there is nothing
+// to compute (past the last route, or a slot past the pool).
+__device__ __forceinline__ const uint8_t *blob_of_row(const FfnI8Args &a, int s) {
+    if (s >= min(__ldg(a.offsets + a.L.E), a.T * a.k)) return nullptr;
     const int e = expert_of_row(a.offsets, a.L.E, s);
-    const int route = __ldg(a.sorted_route + s);
-    const uint8_t *blob = e < a.L.E ? expert_blob(a.L, e) : nullptr;
-    if (blob == nullptr || route < 0 || route >= R) {
-        if (lane == 0) {
-            if (e < a.L.E && blob == nullptr) record_error(0x2005u, (unsigned)__ldg(a.L.slot_table + e));
-            else record_error(0x2007u, (unsigned)s);
-        }
-        return;
-    }
-    const int t = route / a.k;
-    const uint4 *wg = reinterpret_cast<const uint4 *>(blob + a.L.off.q13 + (size_t)i * H);
-    const uint4 *wu = reinterpret_cast<const uint4 *>(blob + a.L.off.q13 + (size_t)(I + i) * H);
-    const uint4 *x = reinterpret_cast<const uint4 *>(a.xq + (size_t)t * H);
-    int ag = 0, au = 0;
-#pragma unroll 4
-    for (int c = lane; c < H / 16; c += 32) {
-        const uint4 xv = __ldg(x + c);
-        ag = dot16(ld_stream_v4(wg + c), xv, ag);
-        au = dot16(ld_stream_v4(wu + c), xv, au);
-    }
-    ag = __reduce_add_sync(kAll, ag);
-    au = __reduce_add_sync(kAll, au);
-    if (lane == 0) {
-        const float *s13 = reinterpret_cast<const float *>(blob + a.L.off.s13);
-        const float sx = __ldg(a.sx + t);
-        h[(size_t)s * I + i] = gate_up(ag, au, sx, __ldg(s13 + i), __ldg(s13 + I + i));
-    }
+    const uint8_t *blob = expert_blob(a.L, e);
+    if (blob == nullptr && (threadIdx.x & 31) == 0) record_error(0x2005u, (unsigned)__ldg(a.L.slot_table + e));
+    return blob;
 }
 
-// Phase 2: a CTA takes 32 output rows of one sorted row; it forms the codes of
-// that row's h in shared memory first.
-constexpr int kRows2 = 32;
-__global__ void __launch_bounds__(32 * kWarps) k_ffn_i8_gemv2(const FfnI8Args a, const float *__restrict__ h) {
-    extern __shared__ __align__(16) int8_t s_hq[];  // [I]
-    __shared__ float s_part[kWarps];
+constexpr int kU = 12;  // 16-byte loads of a lane in flight
+
+// Phase 1: one warp per sorted row and intermediate column: lanes 0..15 take the
+// gate row of W13, lanes 16..31 its up row, 16 bytes a lane and load.  All of a
+// 2816-wide pair's loads are issued before the first product, so the launch is about one
+// round trip to HBM wide.
+__global__ void __launch_bounds__(32 * kWarps, 7) k_ffn_i8_gemv1(const FfnI8Args a, float *__restrict__ h) {
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, I = a.L.I, H = a.L.H;
-    const int per = H / kRows2;
-    const int s = blockIdx.x / per, n0 = (blockIdx.x % per) * kRows2;
+    const int lane = threadIdx.x & 31, l16 = lane & 15, I = a.L.I, H = a.L.H, per = I / kWarps;
+    const int s = blockIdx.x / per, i = (blockIdx.x % per) * kWarps + (threadIdx.x >> 5);
     const int R = a.T * a.k;
-    if (s >= min(__ldg(a.offsets + a.L.E), R)) return;
-    const int e = expert_of_row(a.offsets, a.L.E, s);
-    const uint8_t *blob = e < a.L.E ? expert_blob(a.L, e) : nullptr;
-    if (blob == nullptr) return;  // recorded by phase 1
-    const float *hr = h + (size_t)s * I;
+    const int route = a.T == 1 ? s : __ldg(a.sorted_route + s);
+    const uint8_t *blob = blob_of_row(a, s);
+    if (blob == nullptr) return;
+    if (route < 0 || route >= R) {
+        if (lane == 0) record_error(0x2007u, (unsigned)s);
+        return;
+    }
+    const int t = a.T == 1 ? 0 : route / a.k;
+    const int row = lane < 16 ? i : I + i, nch = H / 16;
+    const uint4 *w = reinterpret_cast<const uint4 *>(blob + a.L.off.q13 + (size_t)row * H) + l16;
+    const uint4 *x = reinterpret_cast<const uint4 *>(a.xq + (size_t)t * H) + l16;
+    const float sw = __ldg(reinterpret_cast<const float *>(blob + a.L.off.s13) + row), sx = __ldg(a.sx + t);
+    int acc = 0;
+    for (int c0 = l16; c0 < nch; c0 += 16 * kU, w += 16 * kU, x += 16 * kU) {
+        uint4 u[kU];
+#pragma unroll
+        for (int j = 0; j < kU; ++j)
+            u[j] = c0 + 16 * j < nch ? ld_stream_v4(w + 16 * j) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int j = 0; j < kU; ++j)
+            if (c0 + 16 * j < nch) acc = dot16(u[j], __ldg(x + 16 * j), acc);
+    }
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) acc += __shfl_xor_sync(kAll, acc, off);
+    const int up = __shfl_xor_sync(kAll, acc, 16);
+    const float su = __shfl_xor_sync(kAll, sw, 16);
+    if (lane == 0) h[(size_t)s * I + i] = gate_up(acc, up, sx, sw, su);
+}
+
+// Phase 2: a CTA takes 32 output rows of one sorted row, four lanes a row.  A lane's
+// first weights are requested before the wait for h (phase 1 has waited for all
+// launches before it, and writes no weights), then the CTA forms the codes of the
+// row's h in shared memory.
+constexpr int kRows2 = 8 * kWarps;
+__global__ void __launch_bounds__(32 * kWarps, 6) k_ffn_i8_gemv2(const FfnI8Args a, const float *__restrict__ h) {
+    extern __shared__ __align__(16) int8_t s_hq[];  // [I]
+    __shared__ float s_part[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, I = a.L.I, H = a.L.H;
+    const int per = H / kRows2, nch = I / 16;
+    const int s = blockIdx.x / per, n = (blockIdx.x % per) * kRows2 + (threadIdx.x >> 2), l4 = lane & 3;
+    const uint8_t *blob = blob_of_row(a, s);
+    if (blob == nullptr) {
+        pdl_wait();
+        return;
+    }
+    const uint4 *w = reinterpret_cast<const uint4 *>(blob + a.L.off.q2 + (size_t)n * I) + l4;
+    uint4 u[kU];
+#pragma unroll
+    for (int j = 0; j < kU; ++j)
+        u[j] = l4 + 4 * j < nch ? ld_stream_v4(w + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
+    const float sw = __ldg(reinterpret_cast<const float *>(blob + a.L.off.s2) + n);
+    pdl_wait();
+    pdl_launch_dependents();
+    const float4 *hr = reinterpret_cast<const float4 *>(h + (size_t)s * I);
     float amax = 0.0f;
-    for (int i = threadIdx.x; i < I; i += 32 * kWarps) amax = fmaxf(amax, fabsf(hr[i]));
+    for (int i = threadIdx.x; i < I / 4; i += 32 * kWarps) {
+        const float4 v = hr[i];
+        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+    }
     amax = warp_max(amax);
     if (lane == 0) s_part[warp] = amax;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_part[w]);
+    for (int i = 0; i < kWarps; ++i) amax = fmaxf(amax, s_part[i]);
     const CodeScale sc = code_scale(amax);
-    const float sh = sc.s;
-    for (int i = threadIdx.x; i < I; i += 32 * kWarps) s_hq[i] = (int8_t)sc.code(hr[i]);
+    for (int i = threadIdx.x; i < I / 4; i += 32 * kWarps) reinterpret_cast<uint32_t *>(s_hq)[i] = sc.code4(hr[i]);
     __syncthreads();
-    const float *s2 = reinterpret_cast<const float *>(blob + a.L.off.s2);
-    for (int n = n0 + warp; n < n0 + kRows2; n += kWarps) {
-        const uint4 *w = reinterpret_cast<const uint4 *>(blob + a.L.off.q2 + (size_t)n * I);
-        int acc = 0;
-        for (int c = lane; c < I / 16; c += 32)
-            acc = dot16(ld_stream_v4(w + c), reinterpret_cast<const uint4 *>(s_hq)[c], acc);
-        acc = __reduce_add_sync(kAll, acc);
-        if (lane == 0) a.rows[(size_t)s * H + n] = scaled(acc, sh, __ldg(s2 + n));
+    const uint4 *x = reinterpret_cast<const uint4 *>(s_hq);
+    int acc = 0;
+    for (int c0 = l4;;) {
+#pragma unroll
+        for (int j = 0; j < kU; ++j)
+            if (c0 + 4 * j < nch) acc = dot16(u[j], x[c0 + 4 * j], acc);
+        c0 += 4 * kU;
+        w += 4 * kU;
+        if (c0 >= nch) break;
+#pragma unroll
+        for (int j = 0; j < kU; ++j)
+            u[j] = c0 + 4 * j < nch ? ld_stream_v4(w + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
     }
+    acc += __shfl_xor_sync(kAll, acc, 1);
+    acc += __shfl_xor_sync(kAll, acc, 2);
+    if (l4 == 0) a.rows[(size_t)s * H + n] = scaled(acc, sc.s, sw);
 }
 
 }  // namespace
