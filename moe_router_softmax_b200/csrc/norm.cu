@@ -1,7 +1,7 @@
 // norm.cu -- the norms around a block: the block's output (dense, or combined
 // from the experts' rows) is normalised, gated and added to the residual, and
 // the sum is normalised again for the next block, whose int8 products may take
-// it as codes.  One CTA per token, the row held in registers throughout.
+// it as codes.  The row is held in registers throughout.
 //
 //   z  = dense z[t], or sum_j w[t][j] rows[route_pos[t k + j]]      (fp32)
 //   zn = z * rsqrt(mean(z^2) + eps) * (offset + post_w)
@@ -32,10 +32,11 @@ __device__ __forceinline__ uint4 pack8(const float v[8]) {
     return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-// Sum or maximum over the CTA, the same on every thread (fixed order: the
-// lanes' butterfly, then the warps in turn).
+// Sum or maximum over a row's threads, the same on every one (fixed order: the
+// lanes' butterfly, then the warps in turn).  Each reduction of a kernel has its own
+// partials, so one barrier serves it.
 template <bool MAX>
-__device__ __forceinline__ float block_reduce(float v, float *s_part) {
+__device__ __forceinline__ float row_reduce(float v, float *s_part) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         const float o = __shfl_xor_sync(0xffffffffu, v, off);
@@ -43,7 +44,6 @@ __device__ __forceinline__ float block_reduce(float v, float *s_part) {
     }
     const int nw = (int)(blockDim.x >> 5);
     if (nw == 1) return v;
-    __syncthreads();  // the previous reduction's partials have been read
     if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
     __syncthreads();
     v = s_part[0];
@@ -51,15 +51,39 @@ __device__ __forceinline__ float block_reduce(float v, float *s_part) {
     return v;
 }
 
-// CH chunks of 8 columns per thread (chunk c on thread c % blockDim).
-template <int SRC, int CH>
-__global__ void __launch_bounds__(1024) k_norm(const NormArgs a) {
-    __shared__ float s_part[32];
+__device__ __forceinline__ void load8(const float *p, float v[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// A row on blockDim.x threads (blockDim.y rows per CTA, more than one only when a
+// row is a warp's), CH chunks of 8 columns per thread (chunk c of the row on thread
+// c % blockDim.x).  The rows are read once and written once.  FEW rows are bound by the
+// chain of loads and reductions: everything that a row needs is requested before its
+// first reduction, and the rows of eight routes at a time.  Many are bound by HBM, where
+// more rows in flight (fewer registers) hide a row's chain.
+constexpr int kMaxThreads = 512;
+template <int SRC, int CH, bool FEW>
+__global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : (SRC == kSrcRows ? 3 : 2)) k_norm(const NormArgs a) {
+    constexpr bool EARLY = (FEW || SRC != kSrcRows) && CH <= 2;
+    constexpr int B = FEW ? 8 : 2;  // routes at a time (many rows: 2 at three CTAs an SM, 147 us; 4 at two, 196)
+    __shared__ float s_part[3][32];
     pdl_wait();
     pdl_launch_dependents();
-    const int t = blockIdx.x, nch = a.H / 8;
+    const int t = blockIdx.x * blockDim.y + threadIdx.y, nch = a.H / 8;
+    if (t >= a.T) return;
     const size_t base = (size_t)t * a.H;
+    const bool post = SRC != kSrcNone && a.post_w != nullptr, next = a.next_w != nullptr;
     float v[CH][8];
+    uint4 res[CH], pw[CH], nw[CH];
+    float gh[CH][8];
+    // the block's weights for chunk c of this thread
+    auto load_block = [&](int c, int ch) {
+        res[c] = reinterpret_cast<const uint4 *>(a.residual + base)[ch];  // a plain load: y may be this row
+        if (post) pw[c] = __ldg(reinterpret_cast<const uint4 *>(a.post_w) + ch);
+        if (a.gate_h) load8(a.gate_h + ch * 8, gh[c]);
+    };
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int ch = threadIdx.x + c * blockDim.x;
@@ -67,74 +91,93 @@ __global__ void __launch_bounds__(1024) k_norm(const NormArgs a) {
         for (int i = 0; i < 8; ++i) v[c][i] = 0.0f;
         if (ch >= nch) continue;
         if (SRC == kSrcRows) {
-            for (int j = 0; j < a.k; ++j) {
-                const int p = __ldg(a.route_pos + (size_t)t * a.k + j);
-                if ((unsigned)p >= (unsigned)(a.T * a.k)) continue;  // a dropped route
-                const float wj = __ldg(a.w + (size_t)t * a.k + j);
-                const float4 *r = reinterpret_cast<const float4 *>(a.rows + (size_t)p * a.H + ch * 8);
-                const float4 r0 = __ldg(r), r1 = __ldg(r + 1);
-                const float rv[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+            for (int j0 = 0; j0 < a.k; j0 += B) {
+                int p[B];
+                float wj[B], r[B][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[c][i] = __fmaf_rn(wj, rv[i], v[c][i]);
+                for (int j = 0; j < B; ++j) {
+                    p[j] = j0 + j < a.k ? __ldg(a.route_pos + (size_t)t * a.k + j0 + j) : -1;
+                    wj[j] = j0 + j < a.k ? __ldg(a.w + (size_t)t * a.k + j0 + j) : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+                    if ((unsigned)p[j] < (unsigned)(a.T * a.k)) load8(a.rows + (size_t)p[j] * a.H + ch * 8, r[j]);
+                if (EARLY && j0 == 0) {
+                    load_block(c, ch);
+                    if (next) nw[c] = __ldg(reinterpret_cast<const uint4 *>(a.next_w) + ch);
+                }
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+                    if ((unsigned)p[j] < (unsigned)(a.T * a.k)) {  // not a dropped route
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[c][i] = __fmaf_rn(wj[j], r[j][i], v[c][i]);
+                    }
             }
         } else {
             const uint16_t *src = SRC == kSrcDense ? a.z : a.residual;
-            unpack8(reinterpret_cast<const uint4 *>(src + base)[ch], v[c]);  // a plain load: y may be this row
+            const uint4 u = reinterpret_cast<const uint4 *>(src + base)[ch];
+            if (EARLY) {
+                if (SRC == kSrcDense) load_block(c, ch);
+                if (next) nw[c] = __ldg(reinterpret_cast<const uint4 *>(a.next_w) + ch);
+            }
+            unpack8(u, v[c]);
         }
     }
     if (SRC != kSrcNone) {
+        const float bs = a.gate_t ? a.block_scale * __ldg(a.gate_t + t) : a.block_scale;
         float r = 1.0f;
-        if (a.post_w) {
+        if (post) {
             float ss = 0.0f;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) ss = __fmaf_rn(v[c][i], v[c][i], ss);
-            r = __frsqrt_rn(block_reduce<false>(ss, s_part) / (float)a.H + a.eps);
+            r = __frsqrt_rn(row_reduce<false>(ss, s_part[0]) / (float)a.H + a.eps);
         }
-        const float bs = a.gate_t ? a.block_scale * __ldg(a.gate_t + t) : a.block_scale;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int ch = threadIdx.x + c * blockDim.x;
             if (ch >= nch) continue;
-            float res[8], pw[8];
-            unpack8(reinterpret_cast<const uint4 *>(a.residual + base)[ch], res);
-            if (a.post_w) unpack8(__ldg(reinterpret_cast<const uint4 *>(a.post_w) + ch), pw);
+            if (!EARLY) load_block(c, ch);
+            float rv[8], wv[8];
+            unpack8(res[c], rv);
+            if (post) unpack8(pw[c], wv);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float zn = v[c][i];
-                if (a.post_w) zn = zn * r * (a.offset + pw[i]);
-                if (a.gate_h) zn *= __ldg(a.gate_h + ch * 8 + i);
-                v[c][i] = a.residual_scale * res[i] + bs * zn;
+                if (post) zn = zn * r * (a.offset + wv[i]);
+                if (a.gate_h) zn *= gh[c][i];
+                v[c][i] = a.residual_scale * rv[i] + bs * zn;
             }
             const uint4 o = pack8(v[c]);
             reinterpret_cast<uint4 *>(a.y + base)[ch] = o;
             unpack8(o, v[c]);  // the next norm reads what is stored
         }
     }
-    if (a.next_w == nullptr) return;
+    if (!next) return;
     float ss = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __fmaf_rn(v[c][i], v[c][i], ss);
-    const float r = __frsqrt_rn(block_reduce<false>(ss, s_part) / (float)a.H + a.eps);
+    const float r = __frsqrt_rn(row_reduce<false>(ss, s_part[1]) / (float)a.H + a.eps);
     float amax = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int ch = threadIdx.x + c * blockDim.x;
         if (ch >= nch) continue;
-        float nw[8];
-        unpack8(__ldg(reinterpret_cast<const uint4 *>(a.next_w) + ch), nw);
+        if (!EARLY) nw[c] = __ldg(reinterpret_cast<const uint4 *>(a.next_w) + ch);
+        float wv[8];
+        unpack8(nw[c], wv);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[c][i] = v[c][i] * r * (a.offset + nw[i]);
+            v[c][i] = v[c][i] * r * (a.offset + wv[i]);
             amax = fmaxf(amax, fabsf(v[c][i]));
         }
         if (a.xn) reinterpret_cast<uint4 *>(a.xn + base)[ch] = pack8(v[c]);
     }
     if (a.xq == nullptr) return;
-    const CodeScale sc = code_scale(block_reduce<true>(amax, s_part));
+    const CodeScale sc = code_scale(row_reduce<true>(amax, s_part[2]));
     if (threadIdx.x == 0) a.sx[t] = sc.s;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -146,13 +189,30 @@ __global__ void __launch_bounds__(1024) k_norm(const NormArgs a) {
     }
 }
 
+// Rows up to 1024 wide: a warp each, four to a CTA.  Wider ones: a CTA each, of a
+// chunk per thread where the row's chain or the routes' loads count, of up to 128
+// threads for many rows without routes (all of 1023 rows resident at once: 18.2 us
+// against 18.6 with 256 threads, with the codes' use behind it).
+// Measured: one token of 8 routes 5.8 -> 4.3 us (FEW); 8192 tokens of 8 routes, 2816
+// wide, 157 -> 147 us, 6.0 TB/s of 876 MB.
+constexpr int kFewRows = 256;
+
+template <int SRC, bool FEW>
+cudaError_t launch_rows(const NormArgs &a, cudaStream_t s) {
+    const int nch = a.H / 8, x_max = nch <= 128 ? 32 : (FEW || SRC == kSrcRows ? kMaxThreads : 128), y = nch <= 128 && a.T >= 4 ? 4 : 1;
+    int ch = 1;
+    while (ch * x_max < nch) ch *= 2;  // 1, 2 or 4 (H <= 16384)
+    const int x = ((nch + ch - 1) / ch + 31) / 32 * 32;
+    const dim3 grid((unsigned)((a.T + y - 1) / y)), block((unsigned)x, (unsigned)y);
+    if (ch == 1) return launch_pdl(k_norm<SRC, 1, FEW>, grid, block, 0, s, a);
+    if (ch == 2) return launch_pdl(k_norm<SRC, 2, FEW>, grid, block, 0, s, a);
+    if (ch == 8) return launch_pdl(k_norm<SRC, 8, FEW>, grid, block, 0, s, a);
+    return launch_pdl(k_norm<SRC, 4, FEW>, grid, block, 0, s, a);
+}
+
 template <int SRC>
 cudaError_t launch_src(const NormArgs &a, cudaStream_t s) {
-    const int nch = a.H / 8;
-    const int ch = (nch + 1023) / 1024;                       // 1 or 2 (H <= 16384)
-    const int threads = (((nch + ch - 1) / ch) + 31) / 32 * 32;
-    if (ch == 1) return launch_pdl(k_norm<SRC, 1>, dim3((unsigned)a.T), dim3((unsigned)threads), 0, s, a);
-    return launch_pdl(k_norm<SRC, 2>, dim3((unsigned)a.T), dim3((unsigned)threads), 0, s, a);
+    return a.T <= kFewRows ? launch_rows<SRC, true>(a, s) : launch_rows<SRC, false>(a, s);
 }
 
 }  // namespace
