@@ -378,7 +378,8 @@ MOE_API moe_status moe_grouped_ffn_w8a8(const moe_layer *layer, const int8_t *xq
  *   xn, xq, sx = moe_norm's of y[t] as stored, with next_w (none without next_w)
  * residual bf16 [T][H]; post_w, next_w bf16 [H], gate_h fp32 [H] and gate_t fp32
  * [T] nullable; y bf16 [T][H] may be residual or z itself.  Means and sums are
- * fp32.  eps > 0; H a multiple of 64 in [64, 16384]; 16-byte aligned pointers
+ * fp32, in an order that H alone decides: a row's results are the same bits in any
+ * batch, and xn, xq and sx those of moe_norm called on y.  eps > 0; H a multiple of 64 in [64, 16384]; 16-byte aligned pointers
  * (sx, gate_t, route_pos and w: 4).
  */
 MOE_API moe_status moe_norm(const uint16_t *x, const uint16_t *weight, int32_t T, int32_t H, float eps, float offset,

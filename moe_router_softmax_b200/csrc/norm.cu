@@ -189,24 +189,23 @@ __global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : (SRC == kSrcR
     }
 }
 
-// Rows up to 1024 wide: a warp each, four to a CTA.  Wider ones: a CTA each, of a
-// chunk per thread where the row's chain or the routes' loads count, of up to 128
-// threads for many rows without routes (all of 1023 rows resident at once: 18.2 us
-// against 18.6 with 256 threads, with the codes' use behind it).
+// Rows up to 1024 wide: a warp each, four to a CTA.  Wider ones: a CTA each, up to
+// 512 threads.  A row's layout, and so the order of its sums, depends on its width
+// alone: a row's result is the same in any batch, and whether the norm before the next
+// block runs here or by itself.
 // Measured: one token of 8 routes 5.8 -> 4.3 us (FEW); 8192 tokens of 8 routes, 2816
 // wide, 157 -> 147 us, 6.0 TB/s of 876 MB.
 constexpr int kFewRows = 256;
 
 template <int SRC, bool FEW>
 cudaError_t launch_rows(const NormArgs &a, cudaStream_t s) {
-    const int nch = a.H / 8, x_max = nch <= 128 ? 32 : (FEW || SRC == kSrcRows ? kMaxThreads : 128), y = nch <= 128 && a.T >= 4 ? 4 : 1;
+    const int nch = a.H / 8, y = nch <= 128 && a.T >= 4 ? 4 : 1, x_max = nch <= 128 ? 32 : kMaxThreads;
     int ch = 1;
     while (ch * x_max < nch) ch *= 2;  // 1, 2 or 4 (H <= 16384)
     const int x = ((nch + ch - 1) / ch + 31) / 32 * 32;
     const dim3 grid((unsigned)((a.T + y - 1) / y)), block((unsigned)x, (unsigned)y);
     if (ch == 1) return launch_pdl(k_norm<SRC, 1, FEW>, grid, block, 0, s, a);
     if (ch == 2) return launch_pdl(k_norm<SRC, 2, FEW>, grid, block, 0, s, a);
-    if (ch == 8) return launch_pdl(k_norm<SRC, 8, FEW>, grid, block, 0, s, a);
     return launch_pdl(k_norm<SRC, 4, FEW>, grid, block, 0, s, a);
 }
 

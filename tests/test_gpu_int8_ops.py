@@ -316,7 +316,7 @@ def check_next(out, y_stored, nw, eps, off):
 
 
 @pytest.mark.parametrize("T,H", [(1, 64), (3, 128), (2, 320), (5, 2816), (1, 4160), (2, 8192), (1, 8256), (2, 16384),
-                                 (300, 192), (33, 1024)])
+                                 (300, 192), (33, 1024), (258, 16384), (300, 8256), (257, 4160)])
 @pytest.mark.parametrize("offset", [0.0, 1.0])
 def test_norm(T, H, offset):
     r = np.random.default_rng([T, H])
@@ -333,6 +333,11 @@ def test_norm(T, H, offset):
     assert torch.equal(moe.moe_norm(xt, wt, eps=1e-5, offset=offset).xn, out.xn)
     if T > 1:
         assert float(out.sx[1]) == 0.0 and (out.xq[1] == 0).all()
+
+
+@pytest.mark.parametrize("T,H,k", [(257, 2816, 0), (257, 2816, 3), (260, 16384, 0), (258, 8256, 1), (300, 192, 9)])
+def test_after_block_many_rows(T, H, k):
+    test_after_block(T, H, "all", k)
 
 
 @pytest.mark.parametrize("T,H", [(1, 64), (3, 192), (4, 2816), (1, 8256), (2, 16384), (70, 256)])
@@ -385,6 +390,17 @@ def test_after_block(T, H, form, k):
         b = res.clone()
         o = moe.moe_combine_norm(dev(rows), dev(pos), dev(w), b, y=b, **kw)
         assert torch.equal(o.y, out.y) and torch.equal(o.xq, out.xq)
+
+
+@pytest.mark.parametrize("H", [192, 2816, 8256])
+def test_norm_rows_do_not_depend_on_the_batch(H):
+    r = np.random.default_rng(H)
+    x, _ = bf16(r.standard_normal((300, H)))
+    w, _ = bf16(r.standard_normal(H))
+    whole = moe.moe_norm(x, w, codes=True)
+    for t in (1, 2, 30):
+        part = moe.moe_norm(x[:t], w, codes=True)
+        assert torch.equal(part.xn, whole.xn[:t]) and torch.equal(part.xq, whole.xq[:t])
 
 
 def test_norm_with_infinities_and_nan():
