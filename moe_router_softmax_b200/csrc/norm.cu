@@ -145,9 +145,10 @@ __global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : (SRC == kSrcR
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float zn = v[c][i];
-                if (post) zn = zn * r * (a.offset + wv[i]);
-                if (a.gate_h) zn *= gh[c][i];
-                v[c][i] = a.residual_scale * rv[i] + bs * zn;
+                // (roundings spelled out: the same in every instantiation)
+                if (post) zn = __fmul_rn(__fmul_rn(zn, r), __fadd_rn(a.offset, wv[i]));
+                if (a.gate_h) zn = __fmul_rn(zn, gh[c][i]);
+                v[c][i] = __fmaf_rn(bs, zn, __fmul_rn(a.residual_scale, rv[i]));
             }
             const uint4 o = pack8(v[c]);
             reinterpret_cast<uint4 *>(a.y + base)[ch] = o;
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : (SRC == kSrcR
         unpack8(nw[c], wv);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[c][i] = v[c][i] * r * (a.offset + wv[i]);
+            v[c][i] = __fmul_rn(__fmul_rn(v[c][i], r), __fadd_rn(a.offset, wv[i]));
             amax = fmaxf(amax, fabsf(v[c][i]));
         }
         if (a.xn) reinterpret_cast<uint4 *>(a.xn + base)[ch] = pack8(v[c]);
