@@ -15,12 +15,15 @@
 // group scores are formed in fp32 with a bound on their error, and where every
 // gap that the result rests on (between consecutive winners, between the last one
 // and the next, between the last kept group and the next) exceeds the two errors,
-// 64 bits would decide alike.  The other tokens, a few in a thousand and all with ties,
-// are done over in 64 bits.  The winners' weights are always formed in 64 bits.
+// 64 bits would decide alike.  Elsewhere, a token or two in a hundred, the candidates
+// are put in order in 64 bits: the experts that no gap separates from the k-th, one
+// to a lane, or the groups; where more than 32 are that close, the whole token.  The
+// winners' weights are always formed in 64 bits.
 //
-// Bound by instruction issue: 8192 tokens of 256 experts in 8 groups read 8.4 MB
-// (1.3 us of HBM), and a warp's k rounds of reductions take a few hundred instructions.
-// 64 bits throughout took 23.9 us there.
+// Bound by the integer pipe and, in a small batch, by the chain of reductions: 8192
+// tokens of 256 experts in 8 groups read 8.4 MB (1.3 us of HBM), and a token takes some
+// 1000 warp instructions.  Measured on B200, 64 bits throughout -> this: one token 5.5
+// -> 3.4 us, 61 tokens of 165 experts 7.9 -> 6.5, 8192 tokens 23.7 -> 15.3.
 #include <math.h>
 
 #include "ops.cuh"
@@ -100,45 +103,72 @@ __device__ __forceinline__ int group_best(const ScoredArgs &a, const Key key[VPL
 // Group of expert e by a multiplication: exact for e < 1024.
 __device__ __forceinline__ uint32_t group_mul(int size) { return ((1u << 22) + size - 1) / size; }
 
+// Softmax denominator of a token in 64 bits.
+__device__ __forceinline__ double denominator(const ScoredArgs &a, const float *row, float m) {
+    double z = 0.0;
+#pragma unroll 8
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+        const float l = __ldg(row + e);
+        const double v = score_of(l, false, m, 1.0);
+        z += is_live(l) ? v : 0.0;
+    }
+    return warp_sum(z);
+}
+
+// 64-bit keys of the lane's experts.  (Scores of masked experts are formed like the
+// others, so that the lane's exponentials run side by side.)
+template <int VPL>
+__device__ __forceinline__ void exact_keys(const ScoredArgs &a, const float *row, float m, uint64_t key[VPL]) {
+    const int lane = threadIdx.x & 31, V = (a.E + 31) / 32;
+    const double z = a.sigmoid ? 1.0 : denominator(a, row, m);
+    float l[VPL], b[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const bool in = i < V && lane * V + i < a.E;
+        l[i] = in ? __ldg(row + lane * V + i) : -INFINITY;
+        b[i] = in && a.bias ? __ldg(a.bias + lane * V + i) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const uint64_t k = choice_key(score_of(l[i], a.sigmoid, m, z) + (double)b[i]);
+        key[i] = is_live(l[i]) && is_live(b[i]) ? k : 0;
+    }
+}
+
+// The kept groups (a bit each), decided in 64 bits.
+template <int VPL>
+__device__ __forceinline__ uint32_t exact_groups(const ScoredArgs &a, const uint64_t key[VPL], uint64_t *sk) {
+    uint64_t k1, k2;
+    int per;
+    const int g = group_best<VPL>(a, key, sk, &k1, &k2, &per);
+    uint64_t gk = 0;  // the group's key, on its first lane
+    if ((threadIdx.x & 31) % per == 0 && k1 != 0)
+        gk = choice_key(key_choice(k1) + (a.group_top > 1 && k2 != 0 ? key_choice(k2) : 0.0));
+    uint32_t kept = 0;
+    for (int r = 0; r < a.topk_group; ++r) {
+        const uint64_t best = warp_max_key(gk);
+        if (best == 0) break;  // only groups without a live expert are left
+        const int win = __reduce_min_sync(kAll, gk == best ? g : 32);
+        if (g == win) gk = 0;
+        kept |= 1u << win;
+    }
+    return kept;
+}
+template <int VPL>
+__device__ __noinline__ uint32_t groups_exact(const ScoredArgs &a, const float *row, float m, uint64_t *sk) {
+    uint64_t key[VPL];
+    exact_keys<VPL>(a, row, m, key);
+    return exact_groups<VPL>(a, key, sk);
+}
+
 // One token in 64 bits; returns the expert of place `lane`, or -1.
 template <int VPL>
 __device__ __noinline__ int route_exact(const ScoredArgs &a, const float *row, float m, uint64_t *sk) {
     const int lane = threadIdx.x & 31, V = (a.E + 31) / 32;
-    double z = 1.0;
-    if (!a.sigmoid) {
-        z = 0.0;
-        for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            const float l = e < a.E ? __ldg(row + e) : -INFINITY;
-            if (is_live(l)) z += score_of(l, false, m, 1.0);
-        }
-        z = warp_sum(z);
-    }
     uint64_t key[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane * V + i;
-        key[i] = 0;
-        if (i >= V || e >= a.E) continue;
-        const float l = __ldg(row + e), b = a.bias ? __ldg(a.bias + e) : 0.0f;
-        if (is_live(l) && is_live(b)) key[i] = choice_key(score_of(l, a.sigmoid, m, z) + (double)b);
-    }
+    exact_keys<VPL>(a, row, m, key);
     if (a.n_group > 1) {
-        uint64_t k1, k2;
-        int per;
-        const int g = group_best<VPL>(a, key, sk, &k1, &k2, &per);
-        uint64_t gk = 0;  // the group's key, on its first lane
-        if (lane % per == 0 && k1 != 0)
-            gk = choice_key(key_choice(k1) + (a.group_top > 1 && k2 != 0 ? key_choice(k2) : 0.0));
-        uint32_t kept = 0;
-        for (int r = 0; r < a.topk_group; ++r) {
-            const uint64_t best = warp_max_key(gk);
-            if (best == 0) break;  // only groups without a live expert are left
-            const int win = __reduce_min_sync(kAll, gk == best ? g : 32);
-            if (g == win) gk = 0;
-            kept |= 1u << win;
-        }
-        const uint32_t mul = group_mul(a.group_size);
+        const uint32_t kept = exact_groups<VPL>(a, key, sk), mul = group_mul(a.group_size);
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
             if (!((kept >> (((uint32_t)(lane * V + i) * mul) >> 22)) & 1u)) key[i] = 0;
@@ -166,25 +196,32 @@ __device__ __noinline__ int route_exact(const ScoredArgs &a, const float *row, f
     return mine;
 }
 
-// fp32 choices.  A score s in [0, 1] formed with the fast exponential and division is
-// off by less than 2^-19: sigmoid, s (1 - s) times the exponential's 2 + 1.2 |l| steps,
-// and 2 steps of the division; softmax, s times the steps of its exponential (weighed by
-// it), of the sum (their mean, and VPL + 5 roundings) and of the division, below 60 half
-// steps together.  Adding the bias rounds by half a step of c.  So two choices whose gap
-// exceeds 2^-17 + 2^-21 (|c| + |c'|), four times those bounds, stand in the same
-// order in 64 bits; for group scores, sums of two, twice that.
-__device__ __forceinline__ bool far_apart(float c, float d, float times) {
-    return c - d > times * (0x1p-17f + 0x1p-21f * (fabsf(c) + fabsf(d)));  // false for a NaN (inf - inf)
+// fp32 choices.  What the fast exponential and division (2 + 1.2 |x| and 2 units in
+// the last place, 2^-23 relative) and the roundings leave in a score s:
+//   sigmoid  s (1 - s) (2 + 1.2 |l|) + 0.5 s + 2 s units, below 2^-21
+//   softmax  s times its exponential's error, weighed by it (2 units), the sum's (a
+//            mean of such errors, 4, and up to 37 roundings) and the division's: below
+//            28 units, 2^-18.2
+// Adding the bias rounds by half a unit of c, and a key gives up the bits that hold
+// its slot (below VPL units).  Two choices whose gap exceeds twice the sum of both errors
+// stand in the same order in 64 bits; for group scores, sums of two, twice that again.
+template <int VPL>
+__device__ __forceinline__ bool far_apart(float c, float d, bool sigmoid, float times) {
+    const float score = sigmoid ? 0x1p-19f : 0x1p-16f, rel = 2.0f * (VPL + 1) * 0x1p-23f;
+    return c - d > times * (score + rel * (fabsf(c) + fabsf(d)));  // false for a NaN (inf - inf)
 }
 __device__ __forceinline__ uint32_t key32(float c) {  // of a number that is not NaN; never 0
     const uint32_t b = __float_as_uint(c + 0.0f);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float choice32(uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 
-// Lane l holds experts l V .. l V + V-1, V = ceil(E / 32) <= VPL.
+// Lane l holds experts l V .. l V + V-1, V = ceil(E / 32) <= VPL.  The integer pipe
+// (compares, selects, minima) bounds a prefill batch, so a key holds its slot in its
+// lowest bits: the best of a lane is VPL - 1 maxima, the warp's best one reduction and
+// one vote, and equal choices, which this order would get wrong, are never far apart.
 template <int VPL>
 __global__ void __launch_bounds__(32 * kWarps) k_route_scored(const ScoredArgs a) {
     extern __shared__ uint64_t s_keys[];  // [kWarps][E] with groups
@@ -196,44 +233,62 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_scored(const ScoredArgs a
     const int V = (a.E + 31) / 32, e0 = lane * V;
     const float *row = a.logits + (size_t)t * a.E;
     uint64_t *sk = s_keys + (size_t)warp * a.E;
-    float c[VPL];
+    float c[VPL], b[VPL];
+    // whole 16-byte pieces where every lane's experts are aligned ones
+    if (VPL >= 4 && a.E == 32 * VPL && (((uintptr_t)a.logits | (uintptr_t)a.bias) & 15) == 0) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) c[i] = i < V && e0 + i < a.E ? __ldg(row + e0 + i) : -INFINITY;
-    float m = 0.0f, rz = 1.0f;
-    uint32_t live = 0;
+        for (int i = 0; i < VPL / 4; ++i) {
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(row + e0) + i);
+            const float4 w = a.bias ? __ldg(reinterpret_cast<const float4 *>(a.bias + e0) + i)
+                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) live |= (uint32_t)is_live(c[i]) << i;
+            for (int j = 0; j < 4; ++j) {
+                c[4 * i + j < VPL ? 4 * i + j : 0] = us[j];
+                b[4 * i + j < VPL ? 4 * i + j : 0] = ws[j];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const bool in = i < V && e0 + i < a.E;
+            c[i] = in ? __ldg(row + e0 + i) : -INFINITY;
+            b[i] = in && a.bias ? __ldg(a.bias + e0 + i) : 0.0f;
+        }
+    }
+    uint32_t key[VPL];
+    float m = 0.0f;
     if (a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) c[i] = __fdividef(1.0f, 1.0f + __expf(-c[i]));
+        for (int i = 0; i < VPL; ++i) {
+            const float v = __fdividef(1.0f, 1.0f + __expf(-c[i])) + b[i];
+            key[i] = is_live(c[i]) && is_live(b[i]) ? (key32(v) & ~(uint32_t)(VPL - 1)) | (uint32_t)i : 0u;
+        }
     } else {
         m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) m = (live >> i) & 1u ? fmaxf(m, c[i]) : m;
+        for (int i = 0; i < VPL; ++i) m = is_live(c[i]) ? fmaxf(m, c[i]) : m;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
-        float z = 0.0f;
+        float z = 0.0f, x[VPL];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            c[i] = (live >> i) & 1u ? (c[i] == m ? 1.0f : __expf(c[i] - m)) : 0.0f;
-            z += c[i];
+            x[i] = is_live(c[i]) ? (c[i] == m ? 1.0f : __expf(c[i] - m)) : 0.0f;
+            z += x[i];
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(kAll, z, off);
-        rz = __fdividef(1.0f, z);
-    }
-    uint32_t key[VPL];
+        const float rz = __fdividef(1.0f, z);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const float b = a.bias && i < V && e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.0f;
-        key[i] = ((live >> i) & 1u) && is_live(b) ? key32(c[i] * rz + b) : 0u;
+        for (int i = 0; i < VPL; ++i)
+            key[i] = is_live(c[i]) && is_live(b[i]) ? (key32(x[i] * rz + b[i]) & ~(uint32_t)(VPL - 1)) | (uint32_t)i : 0u;
     }
-    bool sure = true;
+
     if (a.n_group > 1) {
         uint32_t k1 = 0, k2 = 0;
         int g, per;
-        if (a.E == 32 * V && (a.n_group & (a.n_group - 1)) == 0) {
-            // a group is a power of two of whole lanes
+        const bool whole = a.E == 32 * V && (a.n_group & (a.n_group - 1)) == 0;
+        if (whole) {  // a group is a power of two of whole lanes
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
                 k2 = max(k2, min(k1, key[i]));
@@ -247,63 +302,90 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_scored(const ScoredArgs a
         }
         uint32_t gk = 0;
         if (lane % per == 0 && k1 != 0) gk = key32(choice32(k1) + (a.group_top > 1 && k2 != 0 ? choice32(k2) : 0.0f));
-        uint32_t kept = 0;
-        float last = 0.0f;
+        uint32_t kept = 0, last = 0;
         for (int r = 0; r <= a.topk_group; ++r) {
             const uint32_t best = __reduce_max_sync(kAll, gk);
             if (best == 0) break;
             if (r == a.topk_group) {
-                sure = far_apart(last, choice32(best), 2.0f);
+                if (!far_apart<VPL>(choice32(last), choice32(best), a.sigmoid, 2.0f))
+                    kept = groups_exact<VPL>(a, row, m, sk);
                 break;
             }
-            const int win = __reduce_min_sync(kAll, gk == best ? g : 32);
-            if (g == win) gk = 0;
-            kept |= 1u << win;
-            last = choice32(best);
+            const uint32_t who = __ballot_sync(kAll, gk == best);
+            const int win = __ffs(who) - 1;  // equal groups at the border are not far apart
+            if (lane == win) gk = 0;
+            kept |= 1u << (win / per);
+            last = best;
         }
-        const uint32_t mul = group_mul(a.group_size);
+        if (whole) {
+            const bool on = (kept >> g) & 1u;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (!((kept >> (((uint32_t)(e0 + i) * mul) >> 22)) & 1u)) key[i] = 0;
-    }
-
-    int mine = -1;  // lane j: the expert of place j
-    float prev = 0.0f;
-    for (int j = 0; j <= a.k && sure; ++j) {
-        uint32_t bk = key[0];
-        int bi = 0;
-#pragma unroll
-        for (int i = 1; i < VPL; ++i)
-            if (key[i] > bk) {
-                bk = key[i];
-                bi = i;
-            }
-        const uint32_t best = __reduce_max_sync(kAll, bk);
-        if (best == 0) break;  // every live expert of the kept groups is taken
-        const float now = choice32(best);
-        if (j > 0) sure = far_apart(prev, now, 1.0f);
-        if (j == a.k) break;
-        prev = now;
-        const int id = e0 + bi, win = __reduce_min_sync(kAll, bk == best ? id : 0x7fffffff);
-        if (bk == best && id == win) {
+            for (int i = 0; i < VPL; ++i) key[i] = on ? key[i] : 0u;
+        } else {
+            const uint32_t mul = group_mul(a.group_size);
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                if (i == bi) key[i] = 0;
+                if (!((kept >> (((uint32_t)(e0 + i) * mul) >> 22)) & 1u)) key[i] = 0;
         }
-        if (lane == j) mine = win;
     }
-    if (!sure) mine = route_exact<VPL>(a, row, m, sk);
 
-    // weights.  The softmax denominator cancels where they are renormalised
-    double z = 1.0;
-    if (!a.sigmoid && !a.renorm) {
-        z = 0.0;
+    // k rounds, and more until a gap separates the candidates from the rest: lane j
+    // holds the j-th best key and the expert it stands for
+    uint32_t my_key = 0, last = 0;
+    int mine = -1, n = 0;  // n candidates
+    bool sure = true;
+    for (;; ++n) {
+        uint32_t bk = key[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) bk = max(bk, key[i]);
+        const uint32_t best = __reduce_max_sync(kAll, bk);
+        if (best == 0) break;  // every live expert of the kept groups is taken
+        if (n >= a.k && far_apart<VPL>(choice32(last), choice32(best), a.sigmoid, 1.0f)) break;
+        if (n == 32) {
+            sure = false;
+            break;
+        }
+        if (n == a.k - 1) last = best;  // (a later candidate has to be far from place k, not from the one before)
+        const int win = __ffs(__ballot_sync(kAll, bk == best)) - 1, slot = (int)(best & (VPL - 1));
+        if (lane == n) {
+            my_key = best;
+            mine = win * V + slot;
+        }
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if ((live >> i) & 1u) z += score_of(__ldg(row + e0 + i), false, m, 1.0);
-        z = warp_sum(z);
+            if (slot == i) key[i] = lane == win ? 0u : key[i];  // one slot, the same on all lanes
     }
-    double s = mine >= 0 ? score_of(__ldg(row + mine), a.sigmoid, m, z) : 0.0;
+    // the softmax denominator in 64 bits, where a choice or a weight needs it
+    double z = 1.0;
+    bool have_z = a.sigmoid != 0;
+    double s = 0.0;
+    if (!sure) {
+        mine = route_exact<VPL>(a, row, m, sk);
+    } else {
+        const uint32_t after = __shfl_down_sync(kAll, my_key, 1);
+        const bool ordered = lane >= min(n, a.k) - 1 || far_apart<VPL>(choice32(my_key), choice32(after), a.sigmoid, 1.0f);
+        if (n > a.k || !__all_sync(kAll, ordered)) {
+            // the candidates' order in 64 bits, one to a lane
+            if (!have_z) z = denominator(a, row, m);
+            have_z = true;
+            uint64_t ck = 0;
+            if (mine >= 0)
+                ck = choice_key(score_of(__ldg(row + mine), a.sigmoid, m, z) + (double)(a.bias ? __ldg(a.bias + mine) : 0.0f));
+            int won = -1;
+            for (int j = 0; j < min(n, a.k); ++j) {
+                const uint64_t best = warp_max_key(ck);
+                const int win = __reduce_min_sync(kAll, ck == best ? mine : 0x7fffffff);
+                if (mine == win) ck = 0;
+                if (lane == j) won = win;
+            }
+            mine = won;
+        }
+    }
+    if (lane >= a.k) mine = -1;
+
+    // weights.  The softmax denominator cancels where they are renormalised
+    if (!a.renorm && !have_z) z = denominator(a, row, m);
+    if (mine >= 0) s = score_of(__ldg(row + mine), a.sigmoid, m, a.renorm ? 1.0 : z);
     if (a.renorm) {
         const double sum = warp_sum(s);
         s = sum > 0.0 ? s / sum : 0.0;

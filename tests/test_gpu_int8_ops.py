@@ -93,6 +93,20 @@ def test_route_scored_masks_and_ties(score, G):
     check_route(lg, k, bias=np.full(E, -np.inf, np.float32), **kw)
 
 
+@pytest.mark.parametrize("E,k,G,tg", [(64, 3, 4, 2), (40, 32, 1, 1), (128, 8, 1, 1), (96, 11, 3, 2)])
+def test_route_scored_many_tokens(E, k, G, tg):
+    """Batches in which a warp takes several tokens, ties and masks among them."""
+    T = 6001
+    r = np.random.default_rng(E)
+    lg = (2 * r.standard_normal((T, E))).astype(np.float32)
+    lg[::7] = np.round(lg[::7])
+    lg[::11, : E // 2] = -np.inf
+    lg[::501] = -np.inf
+    b = (0.1 * r.standard_normal(E)).astype(np.float32)
+    check_route(lg, k, bias=b, score="sigmoid", n_group=G, topk_group=tg, group_top=1 + (G > 1))
+    check_route(lg, k, renorm=False, n_group=G, topk_group=tg)
+
+
 def test_route_scored_decides_in_64_bits():
     """Choices nearer to one another than fp32 tells apart."""
     E = 64
