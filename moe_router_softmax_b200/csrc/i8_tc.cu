@@ -17,6 +17,17 @@
 //            h[s][i] = gelu_tanh(g) * u  (fp32)
 //   phase 2  as linear, per expert, over the codes of h; rows[s][m] = D sh[s] s2[m]
 //
+// The dense product runs on CTA pairs (tcgen05 cta_group::2) where its tiles fill the
+// GPU: M = 256, each CTA holding 128 of the weight rows and half of the tokens, so that
+// a stage brings 32 KB into an SM instead of 48 and six fit instead of four.  The loads of both
+// CTAs report to the leader's barriers, its MMA warp issues for both, and its
+// commits free the slots of both.
+//
+// Measured on B200 (device time): linear 4096 x 8192 x 2816 in 67.5 us, 2.80 POP/s (one
+// CTA per tile: 79; bound by the tensor pipe and power); FFN of 64 tokens (128 experts,
+// hidden 2816, intermediate 704, top-8), combine included, 116 us, 6.4 TB/s of the active
+// experts; of 2047 tokens 293 us.  Pairs gained the phases nothing (292 to 304 us).
+//
 // Persistent CTAs, one per SM; warp 0 TMA producer of the weights, warp 1 TMEM
 // allocation and the MMA issuer, warps 2..9 epilogue (TMEM -> registers ->
 // global; warp w reads lanes 32 (w % 4) ..), warp 10 TMA producer of the tokens.
@@ -77,36 +88,104 @@ struct TcI8Params {
     void *out;                       // y, h or rows
 };
 
-// Called by a whole warp; one lane issues.
+// Called by a whole warp; one lane issues.  CG = 2: for the CTA pair (its leader's
+// warp), M = 256, each CTA holding its half of both operands and of the sums.
+template <int CG>
 __device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "elect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "elect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
+// One arrival on `bar` when the products issued so far are done; CG = 2: on that
+// barrier of both CTAs.
+template <int CG>
 __device__ __forceinline__ void tc_commit_warp(uint64_t *bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-        : "memory");
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "elect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "elect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+            ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+            : "memory");
+}
+// Address of the pair leader's copy of a shared variable.
+__device__ __forceinline__ uint32_t leader_u32(const void *p) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+// Arrival of an epilogue warp on the leader's barrier.  What it orders are TMEM reads
+// (tcgen05.fence); a release at cluster scope would wait for the warp's global
+// stores as well, a microsecond an item.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// TMA boxes into this CTA's shared memory; the barrier `bar` (an address) is its
+// own or, CG = 2, the pair leader's.
+template <int CG>
+__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y, uint64_t pol) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y), "l"(pol)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y), "l"(pol)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void load_3d(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z,
+                                        uint64_t pol) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%3, %4, %5}], [%2], %6;"
+            ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(pol)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%3, %4, %5}], [%2], %6;"
+            ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(pol)
+            : "memory");
 }
 // {x, row, 16-row block, gate or up, blob} box of W13.
-__device__ __forceinline__ void tma_load_5d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int x, int b, int z,
-                                            uint64_t pol) {
+__device__ __forceinline__ void load_5d(void *dst, const CUtensorMap *map, uint32_t bar, int x, int b, int z,
+                                        uint64_t pol) {
     asm volatile(
         "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%3, %4, %5, %4, %6}], [%2], %7;"
-        ::"r"(smem_u32(smem_dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(0), "r"(b), "r"(z), "l"(pol)
+        ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(0), "r"(b), "r"(z), "l"(pol)
         : "memory");
 }
 
 struct Items {
-    int n_act, total, b_rows, a_slots, b_slots;
+    int n_act, total, b_rows, a_slots, b_slots;  // b_rows: of a CTA's token slot
 };
 
 // Slots of the two rings for token blocks of `rows` rows and stages of ATOMS atoms
@@ -116,8 +195,9 @@ struct Items {
 // the weights in flight count for more than the waits (2047 tokens: two atoms 315 us,
 // one 296), and three token slots leave them the rest of the memory.  The dense
 // product's operands both come from L2 and get the same number of slots.
-template <int MODE, int ATOMS>
+template <int MODE, int ATOMS, int CG>
 __device__ __forceinline__ void split_ring(int rows, Items *it) {
+    rows /= CG;  // a CTA of a pair holds half of the token rows
     const int a = ATOMS * (int)kABytes, b = ATOMS * rows * kKB, even = min(kMaxStages, kRing / (a + b));
     it->b_rows = rows;
     it->b_slots = MODE < kPhase1 || rows <= 64 ? even : 4 - ATOMS;
@@ -126,11 +206,12 @@ __device__ __forceinline__ void split_ring(int rows, Items *it) {
 constexpr int kFewRoutes = 32;  // two atoms a stage up to so many routes per expert on average
 
 // Blocks of an expert's n routes: as few as kNMax allows, of even size, a
-// multiple of 16 (the MMA's N).
+// multiple of 16 (the MMA's N; of 32 for a CTA pair).
 __host__ __device__ __forceinline__ int blocks_of(int n) { return (n + kNMax - 1) / kNMax; }
+template <int CG>
 __host__ __device__ __forceinline__ int block_rows(int n) {
-    const int nb = blocks_of(n);
-    return ((n + nb - 1) / nb + 15) & ~15;
+    const int nb = blocks_of(n), step = 16 * CG;
+    return ((n + nb - 1) / nb + step - 1) / step * step;
 }
 
 // Up to 32 columns of one output row, `stride` values apart (whole chunks without
@@ -159,7 +240,7 @@ struct TokenMaps {
     CUtensorMap m[4];
 };
 
-template <int MODE, int ATOMS>
+template <int MODE, int ATOMS, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CUtensorMap map_pool,
         const __grid_constant__ TokenMaps map_b, const TcI8Params p) {
@@ -178,7 +259,12 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
 
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m_tiles = MODE == kPhase1 ? p.M / 64 : (p.M + kM - 1) / kM;
+    // A CTA's tile: 128 rows of the weights (64 columns of h in phase 1).  A pair takes
+    // two neighbouring ones; rank: which of them (the leader's is 0).  (The item loops
+    // read blockIdx and gridDim themselves: from variables they ran 4% slower.)
+    constexpr int kRows = MODE == kPhase1 ? 64 : kM;
+    const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;
+    const int m_tiles = (p.M + CG * kRows - 1) / (CG * kRows);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -189,16 +275,23 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], kEpiWarps);
+            mbar_init(&tempty[i], CG * kEpiWarps);
         }
         s_abort = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
-                     "r"(kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (CG == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                         "r"(kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                         "r"(kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
     }
     // dense: one expert that holds every token.  phases: the experts with routes
     if (MODE >= kPhase1) {
@@ -206,7 +299,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         __syncthreads();
     }
     if (warp == 0) {
-        int n_act = 0, run = 0, rows = 16;
+        int n_act = 0, run = 0, rows = 16 * CG;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
             const int n = e < p.E ? (MODE < kPhase1 ? p.R : s_cnt[e]) : 0;
@@ -215,7 +308,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             const bool act = n > 0;
             const unsigned m = __ballot_sync(kAll, act);
             const int items = act ? m_tiles * blocks_of(n) : 0;
-            if (act) rows = max(rows, block_rows(n));
+            if (act) rows = max(rows, block_rows<CG>(n));
             int inc = items;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -226,7 +319,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                 const int pos = n_act + __popc(m & ((1u << lane) - 1u));
                 s_act[pos] = (uint16_t)e;
                 s_cnt[pos] = n;
-                s_blk[pos] = (uint16_t)block_rows(n);
+                s_blk[pos] = (uint16_t)block_rows<CG>(n);
                 s_row0[pos] = off;
                 s_base[pos] = run + inc - items;
             }
@@ -238,11 +331,12 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             s_base[n_act] = run;
             s_items.n_act = n_act;
             s_items.total = run;
-            split_ring<MODE, ATOMS>(rows, &s_items);
+            split_ring<MODE, ATOMS, CG>(rows, &s_items);
         }
     }
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();  // the other CTA's barriers are set up
     tc_fence_after();
     // the next launch may take over SMs as this grid's CTAs finish
     pdl_launch_dependents();
@@ -270,7 +364,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         r.e = s_act[cur];
         r.row0 = s_row0[cur] + first;
         r.n = min(blk, s_cnt[cur] - first);
-        r.n_mma = (max(r.n, 1) + 15) & ~15;
+        r.n_mma = (max(r.n, 1) + 16 * CG - 1) & ~(16 * CG - 1);
         r.z = 0;
         r.pool = false;
         if (MODE >= kPhase1) {
@@ -285,7 +379,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             }
             if (bad) {  // nothing is written for it; its weights are read from home
                 r.n = 0;
-                r.n_mma = 16;
+                r.n_mma = 16 * CG;
                 r.row0 = 0;
             }
         }
@@ -302,23 +396,25 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             const uint64_t pol = MODE < kPhase1 ? l2_policy_normal() : l2_policy_first();
             int st = 0;
             uint32_t ph = 0;
-            for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
+            for (int item = blockIdx.x / CG; item < total && !s_abort; item += gridDim.x / CG) {
                 const ItemInfo it = decode(item);
                 const CUtensorMap *ma = it.pool ? &map_pool : &map_home;
                 bool ok = true;
                 for (int kk = 0; kk < nk; ++kk) {
                     if (!mbar_wait(&a_empty[st], ph ^ 1, &s_abort)) { ok = false; break; }
                     const int na = atoms_at(kk);
-                    mbar_arrive_expect_tx(&a_full[st], na * kABytes);
+                    const uint32_t bar = CG == 2 ? leader_u32(&a_full[st]) : smem_u32(&a_full[st]);
+                    // a pair's leader expects the bytes of both CTAs
+                    if (rank == 0) mbar_arrive_expect_tx(&a_full[st], CG * na * kABytes);
                     for (int a = 0; a < na; ++a) {
                         uint8_t *dst = ring + st * a_bytes + a * kABytes;
                         const int x = (kk * ATOMS + a) * kKB;
                         if (MODE == kPhase1) {
 #pragma unroll
                             for (int b = 0; b < 4; ++b)
-                                tma_load_5d(dst + b * (kABytes / 4), ma, &a_full[st], x, it.mt * 4 + b, it.z, pol);
+                                load_5d(dst + b * (kABytes / 4), ma, bar, x, it.mt * 4 + b, it.z, pol);
                         } else {
-                            tma_load_3d(dst, ma, &a_full[st], x, it.mt * kM, it.z, pol);
+                            load_3d<CG>(dst, ma, bar, x, (it.mt * CG + rank) * kM, it.z, pol);
                         }
                     }
                     if (++st == SA) { st = 0; ph ^= 1; }
@@ -333,29 +429,31 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             const uint64_t pol = MODE < kPhase1 ? l2_policy_normal() : l2_policy_last();
             int st = 0;
             uint32_t ph = 0;
-            for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
+            for (int item = blockIdx.x / CG; item < total && !s_abort; item += gridDim.x / CG) {
                 const ItemInfo it = decode(item);
-                // dense: the whole block in one box (rows past the last token read as
-                // zeros); phases: boxes of 128, 64, 32 and 16 rows
-                const int rows = MODE < kPhase1 ? s_items.b_rows : it.n_mma;
+                // dense: the CTA's part of the block in one box (rows past the last token read
+                // as zeros); phases: boxes of 128, 64, 32 and 16 rows
+                const int rows = MODE < kPhase1 ? s_items.b_rows : it.n_mma / CG;
+                const int y = it.row0 + rank * (it.n_mma / CG);
                 bool ok = true;
                 for (int kk = 0; kk < nk; ++kk) {
                     if (!mbar_wait(&be[st], ph ^ 1, &s_abort)) { ok = false; break; }
                     const int na = atoms_at(kk);
-                    mbar_arrive_expect_tx(&bf[st], (uint32_t)(na * rows * kKB));
+                    const uint32_t bar = CG == 2 ? leader_u32(&bf[st]) : smem_u32(&bf[st]);
+                    if (rank == 0) mbar_arrive_expect_tx(&bf[st], (uint32_t)(CG * na * rows * kKB));
                     for (int a = 0; a < na; ++a) {
                         uint8_t *dst = ringb + st * b_bytes + a * b_atom;
                         const int x = (kk * ATOMS + a) * kKB;
                         if (MODE < kPhase1) {
-                            tma_load_2d(dst, &map_b.m[0], &bf[st], x, it.row0, pol);
+                            load_2d<CG>(dst, &map_b.m[0], bar, x, y, pol);
                         } else {
                             int j = 0;
                             for (; j + 128 <= rows; j += 128)
-                                tma_load_2d(dst + j * kKB, &map_b.m[3], &bf[st], x, it.row0 + j, pol);
+                                load_2d<CG>(dst + j * kKB, &map_b.m[3], bar, x, y + j, pol);
 #pragma unroll
                             for (int i = 2; i >= 0; --i)
                                 if (rows & (16 << i)) {
-                                    tma_load_2d(dst + j * kKB, &map_b.m[i], &bf[st], x, it.row0 + j, pol);
+                                    load_2d<CG>(dst + j * kKB, &map_b.m[i], bar, x, y + j, pol);
                                     j += 16 << i;
                                 }
                         }
@@ -366,7 +464,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
             }
         }
     } else if (warp == 1) {
-        // -------------------------------------------------- MMA issuer
+        // -------------------------------------------------- MMA issuer (the pair's leader)
         // The whole warp walks the stages and an elected lane issues, so that the
         // descriptors stay in uniform registers.  A wait on a completed phase costs
         // ~130 cycles: the next stage's is tested before this one's products are issued.
@@ -374,14 +472,14 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         uint32_t pa = 0, pb = 0, aph = 0;
         bool ra = false, rb = false;
         const uint64_t desc_a = sw128_desc(smem_u32(ring)), desc_b = sw128_desc(smem_u32(ringb));
-        for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
+        for (int item = blockIdx.x / CG; rank == 0 && item < total && !s_abort; item += gridDim.x / CG) {
             const ItemInfo it = decode(item);
             if (!__all_sync(kAll, mbar_wait(&tempty[acc], aph ^ 1, &s_abort))) break;
             tc_fence_after();
             const uint32_t d = tmem + (uint32_t)(acc * kNMax);
             // int32 sums, both operands signed 8-bit, N and M of the tile
             const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(it.n_mma >> 3) << 17) |
-                                   ((uint32_t)(kM >> 4) << 24);
+                                   ((uint32_t)((CG * kM) >> 4) << 24);
             bool ok = true;
             for (int kk = 0; kk < nk; ++kk) {
                 if (!__all_sync(kAll, ra) && !__all_sync(kAll, mbar_wait(&a_full[sa], pa, &s_abort))) { ok = false; break; }
@@ -405,18 +503,18 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                     if (left >= kKB) {
 #pragma unroll
                         for (int j = 0; j < kKB / 32; ++j)
-                            tc_mma_i8(d, ada + (uint64_t)(2 * j), bda + (uint64_t)(2 * j), idesc, (kk | a | j) != 0);
+                            tc_mma_i8<CG>(d, ada + (uint64_t)(2 * j), bda + (uint64_t)(2 * j), idesc, (kk | a | j) != 0);
                     } else {
                         const int steps = (left + 31) / 32;  // past K both operands hold zeros
                         for (int j = 0; j < steps; ++j)
-                            tc_mma_i8(d, ada + (uint64_t)(2 * j), bda + (uint64_t)(2 * j), idesc, (kk | a | j) != 0);
+                            tc_mma_i8<CG>(d, ada + (uint64_t)(2 * j), bda + (uint64_t)(2 * j), idesc, (kk | a | j) != 0);
                     }
                 }
-                tc_commit_warp(done_a);
-                if (MODE >= kPhase1) tc_commit_warp(done_b);
+                tc_commit_warp<CG>(done_a);
+                if (MODE >= kPhase1) tc_commit_warp<CG>(done_b);
             }
             if (!ok) break;
-            tc_commit_warp(&tfull[acc]);
+            tc_commit_warp<CG>(&tfull[acc]);
             acc ^= 1;
             aph ^= acc == 0;
         }
@@ -429,10 +527,10 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         uint32_t aph = 0;
         const uint64_t h_pol = l2_policy_last();  // the next launch reads h
         pdl_wait();  // the token rows' scales come from the launch before
-        for (int item = blockIdx.x; item < total && !s_abort; item += gridDim.x) {
+        for (int item = blockIdx.x / CG; item < total && !s_abort; item += gridDim.x / CG) {
             const ItemInfo it = decode(item);
             // output row of this thread, and its scale(s)
-            const int m = MODE == kPhase1 ? it.mt * 64 + q * 16 + (lane & 15) : it.mt * kM + q * 32 + lane;
+            const int m = (it.mt * CG + rank) * kRows + (MODE == kPhase1 ? q * 16 + (lane & 15) : q * 32 + lane);
             float sw = 0.0f, su = 0.0f;
             if (MODE < kPhase1) {
                 if (m < p.M) sw = __ldg(p.wscale + m);
@@ -485,14 +583,19 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
                         v[j + 3] = scaled(raw[j + 3], s4.w, sw);
                     }
                     const size_t at = (size_t)(it.row0 + c0) * p.M + m;
-                    if (m >= p.M) continue;  // a row past the matrix
-                    if (MODE == kLinear) store_cols(static_cast<__nv_bfloat16 *>(p.out) + at, p.M, v, it.n - c0);
-                    else store_cols(static_cast<float *>(p.out) + at, p.M, v, it.n - c0);
+                    if (m < p.M) {  // not a row past the matrix
+                        if (MODE == kLinear) store_cols(static_cast<__nv_bfloat16 *>(p.out) + at, p.M, v, it.n - c0);
+                        else store_cols(static_cast<float *>(p.out) + at, p.M, v, it.n - c0);
+                    }
+                    __syncwarp();
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[acc]);
+            if (lane == 0) {
+                if (CG == 2) mbar_arrive_cluster(leader_u32(&tempty[acc]));
+                else mbar_arrive(&tempty[acc]);
+            }
             acc ^= 1;
             aph ^= acc == 0;
         }
@@ -505,9 +608,13 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
     }
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();  // neither CTA leaves while the other may still signal it
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        if (CG == 1)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
 }
 
@@ -595,15 +702,15 @@ bool encode_w13(CUtensorMap *m, const void *base, uint64_t H, uint64_t I, uint64
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, int ATOMS>
+template <int MODE, int ATOMS, int CG>
 cudaError_t launch_tc(const CUtensorMap &mh, const CUtensorMap &mp, const void *b, const TcI8Params &p, int n_sm,
                       cudaStream_t s) {
     TokenMaps mb;
     for (int i = 0; i < 4; ++i)
         if (!encode_2d(&mb.m[i], b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)p.K, (uint64_t)p.R, kKB,
-                       MODE < kPhase1 ? (uint32_t)block_rows(p.R) : 16u << i, CU_TENSOR_MAP_SWIZZLE_128B))
+                       MODE < kPhase1 ? (uint32_t)block_rows<CG>(p.R) / CG : 16u << i, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
-    auto kern = k_i8_tc<MODE, ATOMS>;
+    auto kern = k_i8_tc<MODE, ATOMS, CG>;
     static bool attr[kMaxDevices] = {};
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -614,7 +721,21 @@ cudaError_t launch_tc(const CUtensorMap &mh, const CUtensorMap &mp, const void *
         if (err != cudaSuccess) return err;
         attr[dev] = true;
     }
-    return launch_pdl(kern, dim3((unsigned)n_sm), dim3(kThreads), kDynSmem, s, mh, mp, mb, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(n_sm / CG * CG));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kDynSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CG;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, mh, mp, mb, p);
 }
 
 size_t a256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -637,7 +758,13 @@ cudaError_t launch_linear_i8_tc(const LinearArgs &a, cudaStream_t s) {
     p.brow = a.sx;
     p.wscale = a.sw;
     p.out = a.y;
-    return a.fp32 ? launch_tc<kLinearF32, 1>(mw, mw, a.xq, p, n_sm, s) : launch_tc<kLinear, 1>(mw, mw, a.xq, p, n_sm, s);
+    // a pair's tiles (256 rows by up to 256 tokens) where they fill the GPU
+    const bool pairs = (int64_t)((a.N + 2 * kM - 1) / (2 * kM)) * blocks_of(a.T) >= n_sm / 2;
+    if (pairs)
+        return a.fp32 ? launch_tc<kLinearF32, 1, 2>(mw, mw, a.xq, p, n_sm, s)
+                      : launch_tc<kLinear, 1, 2>(mw, mw, a.xq, p, n_sm, s);
+    return a.fp32 ? launch_tc<kLinearF32, 1, 1>(mw, mw, a.xq, p, n_sm, s)
+                  : launch_tc<kLinear, 1, 1>(mw, mw, a.xq, p, n_sm, s);
 }
 
 // h fp32 | codes of h | scales of h | gathered codes | gathered scales
@@ -689,7 +816,7 @@ cudaError_t launch_ffn_i8_tc(const FfnI8Args &a, cudaStream_t s) {
     p.brow = ss;
     p.out = h;
     const bool few = (int64_t)R <= (int64_t)E * kFewRoutes;
-    err = few ? launch_tc<kPhase1, 2>(h1, p1, xs, p, n_sm, s) : launch_tc<kPhase1, 1>(h1, p1, xs, p, n_sm, s);
+    err = few ? launch_tc<kPhase1, 2, 1>(h1, p1, xs, p, n_sm, s) : launch_tc<kPhase1, 1, 1>(h1, p1, xs, p, n_sm, s);
     if (err != cudaSuccess) return err;
     const dim3 rows8((unsigned)((R + 7) / 8));
     if (I <= 768) err = launch_pdl(k_codes_h<6>, rows8, dim3(256), 0, s, (const float *)h, a.offsets, E, I, R, hq, sh);
@@ -699,7 +826,7 @@ cudaError_t launch_ffn_i8_tc(const FfnI8Args &a, cudaStream_t s) {
     p.M = H;
     p.brow = sh;
     p.out = a.rows;
-    return few ? launch_tc<kPhase2, 2>(h2, p2, hq, p, n_sm, s) : launch_tc<kPhase2, 1>(h2, p2, hq, p, n_sm, s);
+    return few ? launch_tc<kPhase2, 2, 1>(h2, p2, hq, p, n_sm, s) : launch_tc<kPhase2, 1, 1>(h2, p2, hq, p, n_sm, s);
 }
 
 cudaError_t i8tc_take_error(unsigned *code, unsigned *info) {

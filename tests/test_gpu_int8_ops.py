@@ -156,6 +156,22 @@ def test_linear_int8(T, N, K):
     no_device_error()
 
 
+@pytest.mark.parametrize("T,N,K", [(256, 18944, 128), (257, 18944, 144), (300, 9601, 272), (2000, 2433, 1040),
+                                   (515, 6400, 2816), (4097, 1100, 64)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_linear_int8_large(T, N, K, dtype):
+    """Products that fill the GPU (the exact sums in fp64 on the device)."""
+    g = torch.Generator(DEV).manual_seed(T)
+    xq = torch.randint(-128, 128, (T, K), generator=g, dtype=torch.int8, device=DEV)
+    wq = torch.randint(-128, 128, (N, K), generator=g, dtype=torch.int8, device=DEV)
+    sx, sw = 0.1 + torch.rand(T, generator=g, device=DEV), 0.1 + torch.rand(N, generator=g, device=DEV)
+    y = (xq.double() @ wq.double().t()) * sx.double()[:, None] * sw.double()
+    out = moe.moe_linear_int8(xq, sx, wq, sw, dtype=dtype).double()
+    rel = 3 * ref.U32 if dtype is torch.float32 else ref.UBF * (1 + 3 * ref.U32) + 3 * ref.U32
+    assert bool(((out - y).abs() <= rel * (1 + 1e-6) * y.abs()).all())
+    no_device_error()
+
+
 @pytest.mark.parametrize("T", [1, 4, 40])
 def test_linear_int8_extreme_sums(T):
     """The largest sums int32 has to hold, and rows of zero codes and scales."""
