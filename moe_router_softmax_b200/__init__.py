@@ -543,6 +543,15 @@ def _arg(t, shape, dtype, name: str, dev: int):
     return t.data_ptr()
 
 
+def _out(t, shape, strides, dtype, name: str, dev: int, device):
+    """An output tensor and its address: the caller's, checked, or a new one (the
+    cheapest of torch's ways to make it; these calls are a few microseconds long)."""
+    if t is None:
+        t = torch.empty_strided(shape, strides, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _arg(t, shape, dtype, name, dev)
+
+
 def _device_of(t: torch.Tensor, ndim: int, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -554,7 +563,7 @@ def _device_of(t: torch.Tensor, ndim: int, name: str) -> int:
 def _call(fn, dev: int, stream, *args) -> None:
     """Run an entry point on device `dev`, on `stream` or the device's current stream."""
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -571,11 +580,11 @@ def moe_route_scored(logits: torch.Tensor, k: int, bias: torch.Tensor | None = N
     int32 [T, k] (-1 where a token has fewer than k live experts) and fp32 [T, k]."""
     dev = _device_of(logits, 2, "logits")
     T, E = logits.shape
-    ids = logits.new_empty((T, k), dtype=torch.int32) if ids is None else ids
-    w = logits.new_empty((T, k), dtype=torch.float32) if w is None else w
+    ids, p_ids = _out(ids, (T, k), (k, 1), torch.int32, "ids", dev, logits.device)
+    w, p_w = _out(w, (T, k), (k, 1), torch.float32, "w", dev, logits.device)
     _call(_lib.moe_route_scored, dev, stream, _arg(logits, (T, E), torch.float32, "logits", dev),
           _arg(bias, (E,), torch.float32, "bias", dev), T, E, k, score, n_group, topk_group, group_top, bool(renorm),
-          scale, _arg(ids, (T, k), torch.int32, "ids", dev), _arg(w, (T, k), torch.float32, "w", dev))
+          scale, p_ids, p_w)
     return ids, w
 
 
@@ -586,12 +595,12 @@ def moe_linear_int8(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: to
     dev = _device_of(xq, 2, "xq")
     T, K = xq.shape
     N = wq.shape[0]
-    if y is None:
-        y = xq.new_empty((T, N), dtype=dtype)
+    if y is None and dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"y has dtype {dtype}, expected bfloat16 or float32")
+    y, p_y = _out(y, (T, N), (N, 1), dtype if y is None else (torch.bfloat16, torch.float32), "y", dev, xq.device)
     _call(_lib.moe_linear_int8, dev, stream, _arg(xq, (T, K), torch.int8, "xq", dev),
           _arg(sx, (T,), torch.float32, "sx", dev), _arg(wq, (N, K), torch.int8, "wq", dev),
-          _arg(sw, (N,), torch.float32, "sw", dev), T, N, K,
-          _arg(y, (T, N), (torch.bfloat16, torch.float32), "y", dev), y.dtype is torch.float32)
+          _arg(sw, (N,), torch.float32, "sw", dev), T, N, K, p_y, y.dtype is torch.float32)
     return y
 
 
@@ -629,13 +638,15 @@ class NormOut(NamedTuple):
     sx: Optional[torch.Tensor]  # fp32 [T], their scales
 
 
-def _norm_out(like, T, y, xn, xq, sx, want_xn, codes) -> NormOut:
-    if xn is None and want_xn:
-        xn = torch.empty_like(like)
-    if codes:
-        xq = torch.empty_like(like, dtype=torch.int8) if xq is None else xq
-        sx = like.new_empty((T,), dtype=torch.float32) if sx is None else sx
-    return NormOut(y, xn, xq, sx)
+def _next_outputs(T, H, dev, device, xn, xq, sx, want_xn, codes):
+    """xn, xq, sx and their addresses (None where not asked for)."""
+    p_xn = p_xq = p_sx = None
+    if xn is not None or want_xn:
+        xn, p_xn = _out(xn, (T, H), (H, 1), torch.bfloat16, "xn", dev, device)
+    if codes or xq is not None or sx is not None:
+        xq, p_xq = _out(xq, (T, H), (H, 1), torch.int8, "xq", dev, device)
+        sx, p_sx = _out(sx, (T,), (1,), torch.float32, "sx", dev, device)
+    return xn, xq, sx, p_xn, p_xq, p_sx
 
 
 def moe_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: float = 0.0, codes: bool = False,
@@ -645,25 +656,23 @@ def moe_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: f
     (``want_xn``) and, with ``codes``, as int8 codes with a scale per token."""
     dev = _device_of(x, 2, "x")
     T, H = x.shape
-    o = _norm_out(x, T, None, xn, xq, sx, want_xn, codes)
+    xn, xq, sx, *ptrs = _next_outputs(T, H, dev, x.device, xn, xq, sx, want_xn, codes)
     bf = torch.bfloat16
     _call(_lib.moe_norm, dev, stream, _arg(x, (T, H), bf, "x", dev), _arg(weight, (H,), bf, "weight", dev), T, H, eps,
-          offset, _arg(o.xn, (T, H), bf, "xn", dev), _arg(o.xq, (T, H), torch.int8, "xq", dev),
-          _arg(o.sx, (T,), torch.float32, "sx", dev))
-    return o
+          offset, *ptrs)
+    return NormOut(None, xn, xq, sx)
 
 
 def _after_block(fn, dev, src, T, H, residual, post_weight, gate_h, gate_t, next_weight, eps, offset, residual_scale,
                  block_scale, codes, want_xn, y, xn, xq, sx, stream) -> NormOut:
     bf, fp = torch.bfloat16, torch.float32
-    y = torch.empty_like(residual) if y is None else y
-    o = _norm_out(residual, T, y, xn, xq, sx, want_xn and next_weight is not None, codes)
+    y, p_y = _out(y, (T, H), (H, 1), bf, "y", dev, residual.device)
+    xn, xq, sx, *ptrs = _next_outputs(T, H, dev, residual.device, xn, xq, sx, want_xn and next_weight is not None, codes)
     _call(fn, dev, stream, *src, _arg(residual, (T, H), bf, "residual", dev),
           _arg(post_weight, (H,), bf, "post_weight", dev), _arg(gate_h, (H,), fp, "gate_h", dev),
           _arg(gate_t, (T,), fp, "gate_t", dev), _arg(next_weight, (H,), bf, "next_weight", dev), T, H, eps, offset,
-          residual_scale, block_scale, _arg(y, (T, H), bf, "y", dev), _arg(o.xn, (T, H), bf, "xn", dev),
-          _arg(o.xq, (T, H), torch.int8, "xq", dev), _arg(o.sx, (T,), fp, "sx", dev))
-    return o
+          residual_scale, block_scale, p_y, *ptrs)
+    return NormOut(y, xn, xq, sx)
 
 
 def moe_residual_norm(z: torch.Tensor, residual: torch.Tensor, post_weight: torch.Tensor | None = None,
