@@ -16,8 +16,14 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 4;
-constexpr int kGemvTokens = 8;   // linear: these kernels up to here, then the tensor cores
-constexpr int kGemvRoutes = 32;  // ffn, in routes
+
+// These kernels up to here, then the tensor cores.  Measured on B200, these / those:
+//   linear: 2816 x 2816, 4 tokens 6.9 / 8.5 us; 8192 x 2816, 2 tokens 7.7 / 9.4, 4
+//   tokens 12.8 / 9.5 (every warp reads the tokens' codes again, from L1)
+//   ffn (top-8, 128 experts of 2816 x 704): 40 routes 46.4 / 50.3, 48 routes 53.4 / 52.0
+constexpr int kGemvTokens = 4;
+constexpr int64_t kGemvProducts = 50000000;  // T N K, past one token
+constexpr int kGemvRoutes = 40;
 
 // First problem a kernel of this file recorded (0 = none), read and cleared by
 // moe_take_device_errors(): 0x2005 a slot past the pool, 0x2007 a route out of range.
@@ -34,39 +40,40 @@ __device__ __forceinline__ int dot16(uint4 w, uint4 x, int acc) {
     return __dp4a((int)w.w, (int)x.w, acc);
 }
 
-// One warp per output row n and block of TB tokens.
+// One warp per output row n and up to TB tokens.
 template <int TB, bool FP32>
 __global__ void __launch_bounds__(32 * kWarps) k_linear_i8(const LinearArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int n = blockIdx.x * kWarps + (threadIdx.x >> 5), t0 = blockIdx.y * TB;
+    const int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (n >= a.N) return;
     const int nch = a.K / 16;
     const uint4 *wr = reinterpret_cast<const uint4 *>(a.wq + (size_t)n * a.K);
+    // a lane's loads of the weight row go out together, ahead of the tokens' (from L1/L2)
+    constexpr int U = 6;
     int acc[TB] = {};
-    for (int c0 = lane; c0 < nch; c0 += 128) {
-        uint4 w[4];
+    for (int c0 = lane; c0 < nch; c0 += 32 * U) {
+        uint4 w[U];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < U; ++u)
             w[u] = c0 + 32 * u < nch ? ld_stream_v4(wr + c0 + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < U; ++u)
             if (c0 + 32 * u < nch)
 #pragma unroll
                 for (int t = 0; t < TB; ++t)
-                    if (t0 + t < a.T)
-                        acc[t] = dot16(w[u],
-                                       __ldg(reinterpret_cast<const uint4 *>(a.xq + (size_t)(t0 + t) * a.K) + c0 + 32 * u),
+                    if (t < a.T)
+                        acc[t] = dot16(w[u], __ldg(reinterpret_cast<const uint4 *>(a.xq + (size_t)t * a.K) + c0 + 32 * u),
                                        acc[t]);
     }
     const float sw = __ldg(a.sw + n);
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
         const int sum = __reduce_add_sync(kAll, acc[t]);
-        if (lane != t || t0 + t >= a.T) continue;
-        const float v = scaled(sum, __ldg(a.sx + t0 + t), sw);
-        const size_t at = (size_t)(t0 + t) * a.N + n;
+        if (lane != t || t >= a.T) continue;
+        const float v = scaled(sum, __ldg(a.sx + t), sw);
+        const size_t at = (size_t)t * a.N + n;
         if (FP32) static_cast<float *>(a.y)[at] = v;
         else static_cast<uint16_t *>(a.y)[at] = f32_to_bf16_rne(v);
     }
@@ -191,14 +198,14 @@ __global__ void __launch_bounds__(32 * kWarps, 6) k_ffn_i8_gemv2(const FfnI8Args
 
 cudaError_t launch_linear_i8(const LinearArgs &a, cudaStream_t s) {
     if (a.T == 0) return cudaSuccess;
-    if (a.T > kGemvTokens) return launch_linear_i8_tc(a, s);
+    if (a.T > kGemvTokens || (a.T > 1 && (int64_t)a.T * a.N * a.K > kGemvProducts)) return launch_linear_i8_tc(a, s);
     const dim3 block(32 * kWarps);
-    auto go = [&](auto kern, int tb) {
-        return launch_pdl(kern, dim3((unsigned)((a.N + kWarps - 1) / kWarps), (unsigned)((a.T + tb - 1) / tb)), block, 0,
-                          s, a);
+    auto go = [&](auto kern) {
+        return launch_pdl(kern, dim3((unsigned)((a.N + kWarps - 1) / kWarps)), block, 0, s, a);
     };
-    if (a.T == 1) return a.fp32 ? go(k_linear_i8<1, true>, 1) : go(k_linear_i8<1, false>, 1);
-    return a.fp32 ? go(k_linear_i8<8, true>, 8) : go(k_linear_i8<8, false>, 8);
+    if (a.T == 1) return a.fp32 ? go(k_linear_i8<1, true>) : go(k_linear_i8<1, false>);
+    if (a.T == 2) return a.fp32 ? go(k_linear_i8<2, true>) : go(k_linear_i8<2, false>);
+    return a.fp32 ? go(k_linear_i8<4, true>) : go(k_linear_i8<4, false>);
 }
 
 size_t ffn_i8_workspace(int H, int I, int T, int k) {

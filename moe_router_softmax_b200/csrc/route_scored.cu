@@ -204,11 +204,16 @@ __device__ __noinline__ int route_exact(const ScoredArgs &a, const float *row, f
 //            28 units, 2^-18.2
 // Adding the bias rounds by half a unit of c, and a key gives up the bits that hold
 // its slot (below VPL units).  Two choices whose gap exceeds twice the sum of both errors
-// stand in the same order in 64 bits; for group scores, sums of two, twice that again.
+// stand in the same order in 64 bits.  size: |c| + |d|, and for group scores, sums of
+// two choices that may cancel, twice the largest members' magnitudes; times: 2 there.
 template <int VPL>
-__device__ __forceinline__ bool far_apart(float c, float d, bool sigmoid, float times) {
-    const float score = sigmoid ? 0x1p-19f : 0x1p-16f, rel = 2.0f * (VPL + 1) * 0x1p-23f;
-    return c - d > times * (score + rel * (fabsf(c) + fabsf(d)));  // false for a NaN (inf - inf)
+__device__ __forceinline__ bool far_apart(float c, float d, float size, bool sigmoid, float times) {
+    const float score = sigmoid ? 0x1p-19f : 0x1p-16f, rel = 2.0f * (VPL + 2) * 0x1p-23f;
+    return c - d > times * (score + rel * size);  // false for a NaN (inf - inf)
+}
+template <int VPL>
+__device__ __forceinline__ bool far_apart(float c, float d, bool sigmoid) {
+    return far_apart<VPL>(c, d, fabsf(c) + fabsf(d), sigmoid, 1.0f);
 }
 __device__ __forceinline__ uint32_t key32(float c) {  // of a number that is not NaN; never 0
     const uint32_t b = __float_as_uint(c + 0.0f);
@@ -301,18 +306,24 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_scored(const ScoredArgs a
             g = group_best<VPL>(a, key, reinterpret_cast<uint32_t *>(sk), &k1, &k2, &per);
         }
         uint32_t gk = 0;
-        if (lane % per == 0 && k1 != 0) gk = key32(choice32(k1) + (a.group_top > 1 && k2 != 0 ? choice32(k2) : 0.0f));
+        float size = 0.0f;
+        if (lane % per == 0 && k1 != 0) {
+            const float c1 = choice32(k1), c2 = a.group_top > 1 && k2 != 0 ? choice32(k2) : 0.0f;
+            gk = c1 + c2 == c1 + c2 ? key32(c1 + c2) : 0xffffffffu;  // (inf - inf: first, and not far from any)
+            size = fabsf(c1) + fabsf(c2);
+        }
+        // the largest members of any group: a sum that cancels carries their errors
+        const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
         uint32_t kept = 0, last = 0;
         for (int r = 0; r <= a.topk_group; ++r) {
             const uint32_t best = __reduce_max_sync(kAll, gk);
             if (best == 0) break;
+            const int win = __ffs(__ballot_sync(kAll, gk == best)) - 1;  // equal groups are not far apart
             if (r == a.topk_group) {
-                if (!far_apart<VPL>(choice32(last), choice32(best), a.sigmoid, 2.0f))
+                if (!far_apart<VPL>(choice32(last), choice32(best), 2.0f * most, a.sigmoid, 2.0f))
                     kept = groups_exact<VPL>(a, row, m, sk);
                 break;
             }
-            const uint32_t who = __ballot_sync(kAll, gk == best);
-            const int win = __ffs(who) - 1;  // equal groups at the border are not far apart
             if (lane == win) gk = 0;
             kept |= 1u << (win / per);
             last = best;
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_scored(const ScoredArgs a
         for (int i = 1; i < VPL; ++i) bk = max(bk, key[i]);
         const uint32_t best = __reduce_max_sync(kAll, bk);
         if (best == 0) break;  // every live expert of the kept groups is taken
-        if (n >= a.k && far_apart<VPL>(choice32(last), choice32(best), a.sigmoid, 1.0f)) break;
+        if (n >= a.k && far_apart<VPL>(choice32(last), choice32(best), a.sigmoid)) break;
         if (n == 32) {
             sure = false;
             break;
@@ -363,7 +374,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_scored(const ScoredArgs a
         mine = route_exact<VPL>(a, row, m, sk);
     } else {
         const uint32_t after = __shfl_down_sync(kAll, my_key, 1);
-        const bool ordered = lane >= min(n, a.k) - 1 || far_apart<VPL>(choice32(my_key), choice32(after), a.sigmoid, 1.0f);
+        const bool ordered = lane >= min(n, a.k) - 1 || far_apart<VPL>(choice32(my_key), choice32(after), a.sigmoid);
         if (n > a.k || !__all_sync(kAll, ordered)) {
             // the candidates' order in 64 bits, one to a lane
             if (!have_z) z = denominator(a, row, m);

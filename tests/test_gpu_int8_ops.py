@@ -119,6 +119,23 @@ def test_route_scored_decides_in_64_bits():
         check_route(lg, 2, bias=b + np.float32(1000.0), score=score)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_scored_with_biases_that_cancel(score):
+    """Group scores that are small sums of large choices, and biases of every size."""
+    T, E = 400, 64
+    r = np.random.default_rng(17)
+    lg = (2 * r.standard_normal((T, E))).astype(np.float32)
+    b = np.zeros(E, np.float32)
+    b[0::8], b[1::8] = 3e4, -3e4
+    check_route(lg, 6, bias=b, score=score, n_group=8, topk_group=3, group_top=2)
+    b = (10.0 ** r.uniform(-6, 6, E) * np.where(r.random(E) < 0.5, -1, 1)).astype(np.float32)
+    for G in (1, 4, 8):
+        check_route(lg, 6, bias=b, score=score, n_group=G, topk_group=max(G // 2, 1), group_top=1 + (G > 1))
+    b = np.full(E, 3e38, np.float32)
+    b[E // 2:] = -3e38
+    check_route(lg, 6, bias=b, score=score, n_group=8, topk_group=5, group_top=2)
+
+
 def test_route_scored_feeds_the_permute():
     T, E, k = 21, 48, 4
     r = np.random.default_rng(5)
