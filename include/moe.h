@@ -17,6 +17,10 @@
  *           places experts in VRAM either pinned or in a cache slot);
  *   combine weighted sum of each token's k expert rows back in token order
  *           (remote_experts.cpp, RemoteExperts::finish).
+ * Around int8 experts it also has what a decoder layer does with them: scored
+ * routing (moe_route_scored), int8 x int8 products (moe_linear_int8,
+ * moe_grouped_ffn_w8a8) and the norms around a block (moe_norm,
+ * moe_residual_norm, moe_combine_norm).
  *
  * Conventions (every call):
  *  - Pointers named in a call are DEVICE memory owned by the caller unless the
