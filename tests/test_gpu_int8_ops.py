@@ -157,7 +157,8 @@ def random_codes(r, *shape, full=False):
 
 
 @pytest.mark.parametrize("T", [1, 2, 5, 8, 9, 16, 31, 64, 65, 130, 257])
-@pytest.mark.parametrize("N,K", [(1, 16), (7, 64), (33, 80), (128, 128), (130, 272), (300, 1040), (64, 2816)])
+@pytest.mark.parametrize("N,K", [(1, 16), (7, 64), (33, 80), (128, 128), (130, 272), (300, 1040), (64, 2816), (129, 528),
+                                 (2500, 544), (5000, 1040), (9473, 400)])
 def test_linear_int8(T, N, K):
     r = np.random.default_rng([T, N, K])
     xq, wq = random_codes(r, T, K, full=True), random_codes(r, N, K, full=True)
