@@ -18,11 +18,13 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 4;
 
 // These kernels up to here, then the tensor cores.  Measured on B200, these / those:
-//   linear: 2816 x 2816, 4 tokens 6.9 / 8.5 us; 8192 x 2816, 2 tokens 7.7 / 9.4, 4
-//   tokens 12.8 / 9.5 (every warp reads the tokens' codes again, from L1)
+//   linear: 2816 x 2816, 2 tokens 4.4 / 5.2 us, 4 tokens 6.9 / 5.2; 8192 x 2816, 2
+//   tokens 7.7 / 9.4, 4 tokens 12.8 / 9.4; 1408 x 704, 4 tokens 3.5 / 4.8 (every warp
+//   reads the tokens' codes again, from L1)
 //   ffn (top-8, 128 experts of 2816 x 704): 40 routes 46.4 / 50.3, 48 routes 53.4 / 52.0
-constexpr int kGemvTokens = 4;
-constexpr int64_t kGemvProducts = 50000000;  // T N K, past one token
+constexpr int kGemvTokens = 2;
+constexpr int kGemvTokensSmall = 4;
+constexpr int64_t kGemvProducts = 20000000;  // T N K, past kGemvTokens
 constexpr int kGemvRoutes = 40;
 
 // First problem a kernel of this file recorded (0 = none), read and cleared by
@@ -198,7 +200,8 @@ __global__ void __launch_bounds__(32 * kWarps, 6) k_ffn_i8_gemv2(const FfnI8Args
 
 cudaError_t launch_linear_i8(const LinearArgs &a, cudaStream_t s) {
     if (a.T == 0) return cudaSuccess;
-    if (a.T > kGemvTokens || (a.T > 1 && (int64_t)a.T * a.N * a.K > kGemvProducts)) return launch_linear_i8_tc(a, s);
+    if (a.T > kGemvTokens && (a.T > kGemvTokensSmall || (int64_t)a.T * a.N * a.K > kGemvProducts))
+        return launch_linear_i8_tc(a, s);
     const dim3 block(32 * kWarps);
     auto go = [&](auto kern) {
         return launch_pdl(kern, dim3((unsigned)((a.N + kWarps - 1) / kWarps)), block, 0, s, a);
