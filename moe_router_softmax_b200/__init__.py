@@ -543,11 +543,21 @@ def _arg(t, shape, dtype, name: str, dev: int):
     return t.data_ptr()
 
 
-def _out(t, shape, strides, dtype, name: str, dev: int, device):
-    """An output tensor and its address: the caller's, checked, or a new one (the
-    cheapest of torch's ways to make it; these calls are a few microseconds long)."""
+def _new(shape, strides, dtype, device, stream) -> torch.Tensor:
+    """A new tensor for a call on `stream` (the cheapest of torch's ways to make one;
+    these calls are a few microseconds long).  It comes from that stream's memory, so
+    that neither earlier work on the current stream nor its later release touches it
+    while the call runs."""
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+
+def _out(t, shape, strides, dtype, name: str, dev: int, device, stream):
+    """An output tensor and its address: the caller's, checked, or a new one."""
     if t is None:
-        t = torch.empty_strided(shape, strides, dtype=dtype, device=device)
+        t = _new(shape, strides, dtype, device, stream)
         return t, t.data_ptr()
     return t, _arg(t, shape, dtype, name, dev)
 
@@ -580,8 +590,8 @@ def moe_route_scored(logits: torch.Tensor, k: int, bias: torch.Tensor | None = N
     int32 [T, k] (-1 where a token has fewer than k live experts) and fp32 [T, k]."""
     dev = _device_of(logits, 2, "logits")
     T, E = logits.shape
-    ids, p_ids = _out(ids, (T, k), (k, 1), torch.int32, "ids", dev, logits.device)
-    w, p_w = _out(w, (T, k), (k, 1), torch.float32, "w", dev, logits.device)
+    ids, p_ids = _out(ids, (T, k), (k, 1), torch.int32, "ids", dev, logits.device, stream)
+    w, p_w = _out(w, (T, k), (k, 1), torch.float32, "w", dev, logits.device, stream)
     _call(_lib.moe_route_scored, dev, stream, _arg(logits, (T, E), torch.float32, "logits", dev),
           _arg(bias, (E,), torch.float32, "bias", dev), T, E, k, score, n_group, topk_group, group_top, bool(renorm),
           scale, p_ids, p_w)
@@ -597,7 +607,8 @@ def moe_linear_int8(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: to
     N = wq.shape[0]
     if y is None and dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"y has dtype {dtype}, expected bfloat16 or float32")
-    y, p_y = _out(y, (T, N), (N, 1), dtype if y is None else (torch.bfloat16, torch.float32), "y", dev, xq.device)
+    y, p_y = _out(y, (T, N), (N, 1), dtype if y is None else (torch.bfloat16, torch.float32), "y", dev,
+                  xq.device, stream)
     _call(_lib.moe_linear_int8, dev, stream, _arg(xq, (T, K), torch.int8, "xq", dev),
           _arg(sx, (T,), torch.float32, "sx", dev), _arg(wq, (N, K), torch.int8, "wq", dev),
           _arg(sw, (N,), torch.float32, "sw", dev), T, N, K, p_y, y.dtype is torch.float32)
@@ -618,15 +629,14 @@ def moe_grouped_ffn_w8a8(layer: MoeLayer, xq: torch.Tensor, sx: torch.Tensor, k:
     if layer.home.get_device() != dev:
         raise ValueError(f"the layer is on {layer.home.device}, xq on {xq.device}")
     T, R = xq.shape[0], xq.shape[0] * k
-    if rows is None:
-        rows = xq.new_empty((R, layer.H), dtype=torch.float32)
+    rows, p_rows = _out(rows, (R, layer.H), (layer.H, 1), torch.float32, "rows", dev, xq.device, stream)
     if ws is None:
-        ws = xq.new_empty(max(moe_grouped_ffn_w8a8_workspace(layer, T, k), 16), dtype=torch.uint8)
+        ws = _new((max(moe_grouped_ffn_w8a8_workspace(layer, T, k), 16),), (1,), torch.uint8, xq.device, stream)
     _call(_lib.moe_grouped_ffn_w8a8, dev, stream, layer.ref(), _arg(xq, (T, layer.H), torch.int8, "xq", dev),
           _arg(sx, (T,), torch.float32, "sx", dev), T, k, _arg(counts, (layer.E,), torch.int32, "counts", dev),
           _arg(offsets, (layer.E + 1,), torch.int32, "offsets", dev),
           _arg(sorted_route, (R,), torch.int32, "sorted_route", dev),
-          _arg(rows, (R, layer.H), torch.float32, "rows", dev), _arg(ws, ws.shape, torch.uint8, "ws", dev), ws.numel())
+          p_rows, _arg(ws, ws.shape, torch.uint8, "ws", dev), ws.numel())
     return rows
 
 
@@ -638,14 +648,14 @@ class NormOut(NamedTuple):
     sx: Optional[torch.Tensor]  # fp32 [T], their scales
 
 
-def _next_outputs(T, H, dev, device, xn, xq, sx, want_xn, codes):
+def _next_outputs(T, H, dev, device, stream, xn, xq, sx, want_xn, codes):
     """xn, xq, sx and their addresses (None where not asked for)."""
     p_xn = p_xq = p_sx = None
     if xn is not None or want_xn:
-        xn, p_xn = _out(xn, (T, H), (H, 1), torch.bfloat16, "xn", dev, device)
+        xn, p_xn = _out(xn, (T, H), (H, 1), torch.bfloat16, "xn", dev, device, stream)
     if codes or xq is not None or sx is not None:
-        xq, p_xq = _out(xq, (T, H), (H, 1), torch.int8, "xq", dev, device)
-        sx, p_sx = _out(sx, (T,), (1,), torch.float32, "sx", dev, device)
+        xq, p_xq = _out(xq, (T, H), (H, 1), torch.int8, "xq", dev, device, stream)
+        sx, p_sx = _out(sx, (T,), (1,), torch.float32, "sx", dev, device, stream)
     return xn, xq, sx, p_xn, p_xq, p_sx
 
 
@@ -656,7 +666,7 @@ def moe_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: f
     (``want_xn``) and, with ``codes``, as int8 codes with a scale per token."""
     dev = _device_of(x, 2, "x")
     T, H = x.shape
-    xn, xq, sx, *ptrs = _next_outputs(T, H, dev, x.device, xn, xq, sx, want_xn, codes)
+    xn, xq, sx, *ptrs = _next_outputs(T, H, dev, x.device, stream, xn, xq, sx, want_xn, codes)
     bf = torch.bfloat16
     _call(_lib.moe_norm, dev, stream, _arg(x, (T, H), bf, "x", dev), _arg(weight, (H,), bf, "weight", dev), T, H, eps,
           offset, *ptrs)
@@ -666,8 +676,9 @@ def moe_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: f
 def _after_block(fn, dev, src, T, H, residual, post_weight, gate_h, gate_t, next_weight, eps, offset, residual_scale,
                  block_scale, codes, want_xn, y, xn, xq, sx, stream) -> NormOut:
     bf, fp = torch.bfloat16, torch.float32
-    y, p_y = _out(y, (T, H), (H, 1), bf, "y", dev, residual.device)
-    xn, xq, sx, *ptrs = _next_outputs(T, H, dev, residual.device, xn, xq, sx, want_xn and next_weight is not None, codes)
+    y, p_y = _out(y, (T, H), (H, 1), bf, "y", dev, residual.device, stream)
+    xn, xq, sx, *ptrs = _next_outputs(T, H, dev, residual.device, stream, xn, xq, sx,
+                                            want_xn and next_weight is not None, codes)
     _call(fn, dev, stream, *src, _arg(residual, (T, H), bf, "residual", dev),
           _arg(post_weight, (H,), bf, "post_weight", dev), _arg(gate_h, (H,), fp, "gate_h", dev),
           _arg(gate_t, (T,), fp, "gate_t", dev), _arg(next_weight, (H,), bf, "next_weight", dev), T, H, eps, offset,

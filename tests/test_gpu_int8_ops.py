@@ -567,6 +567,37 @@ def test_run_together_replayed_and_on_other_streams(T):
     no_device_error()
 
 
+@pytest.mark.parametrize("T", [2, 60])
+def test_calls_on_a_given_stream(T):
+    """`stream=`: results as on the current one, with outputs and workspace made by the
+    call, while the current stream keeps allocating and writing."""
+    E, H, I, k = 8, 256, 128, 2
+    L, _ = int8_layer(E, H, I, seed=41)
+    g = torch.Generator(DEV).manual_seed(T)
+    x = torch.randn(T, H, device=DEV, generator=g).bfloat16()
+    nw = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    lg = torch.randn(T, E, device=DEV, generator=g)
+
+    def run(stream):
+        h = moe.moe_norm(x, nw, codes=True, stream=stream)
+        y = moe.moe_linear_int8(h.xq, h.sx, h.xq, h.sx, stream=stream)
+        ids, w = moe.moe_route_scored(lg, k, stream=stream)
+        counts, offsets, srt, rp = perm if stream is not None else moe.moe_permute(ids, E)
+        rows = moe.moe_grouped_ffn_w8a8(L, h.xq, h.sx, k, counts, offsets, srt, stream=stream)
+        end = moe.moe_combine_norm(rows, rp, w, x, nw, next_weight=nw, codes=True, stream=stream)
+        return [h.xn, h.xq, h.sx, y, ids, w, end.y, end.xn, end.xq, end.sx], (counts, offsets, srt, rp)
+
+    want, perm = run(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        got, _ = run(side)
+        noise = [torch.full((T, H), 3.0, device=DEV) for _ in range(8)]  # what the current stream does meanwhile
+        del noise
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_run_together_against_the_formulas():
     """One block, each step held to its reference on the step's own inputs."""
     T, E, H, I, k = 9, 16, 256, 128, 4
