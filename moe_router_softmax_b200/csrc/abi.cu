@@ -469,7 +469,9 @@ static moe_status block_norm(const NormArgs &a, bool block, const char *what, mo
     CHECK_ARG(aligned16(a.rows) && aligned16(a.z) && aligned16(a.residual) && aligned16(a.post_w) &&
                   aligned16(a.next_w) && aligned16(a.gate_h) && aligned16(a.y) && aligned16(a.xn) && aligned16(a.xq),
               "%s: matrices, norm weights and gate_h must be 16-byte aligned", what);
-    return cuda_status(launch_block_norm(a, (cudaStream_t)stream), what);
+    NormArgs b = a;
+    b.inv_h = 1.0f / (float)a.H;
+    return cuda_status(launch_block_norm(b, (cudaStream_t)stream), what);
 }
 
 moe_status moe_norm(const uint16_t *x, const uint16_t *weight, int32_t T, int32_t H, float eps, float offset,
@@ -494,7 +496,7 @@ moe_status moe_residual_norm(const uint16_t *z, const uint16_t *residual, const 
                              moe_stream_t stream) {
     CHECK_ARG(T <= 0 || z, "moe_residual_norm: NULL pointer");
     const NormArgs a{nullptr, nullptr, nullptr, 0, z, residual, post_w, next_w, gate_h, gate_t, eps, offset,
-                     residual_scale, block_scale, T, H, y, xn, xq, sx};
+                     residual_scale, block_scale, T, H, y, xn, xq, sx, 0.0f};
     return block_norm(a, true, "moe_residual_norm", stream);
 }
 
@@ -507,7 +509,7 @@ moe_status moe_combine_norm(const float *rows, const int32_t *route_pos, const f
     if (st != MOE_OK) return st;
     CHECK_ARG(T == 0 || (rows && route_pos && w), "moe_combine_norm: NULL pointer");
     const NormArgs a{rows, route_pos, w, k, nullptr, residual, post_w, next_w, gate_h, gate_t, eps, offset,
-                     residual_scale, block_scale, T, H, y, xn, xq, sx};
+                     residual_scale, block_scale, T, H, y, xn, xq, sx, 0.0f};
     return block_norm(a, true, "moe_combine_norm", stream);
 }
 

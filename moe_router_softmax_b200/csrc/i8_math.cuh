@@ -25,18 +25,23 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // Scale of a row from its largest magnitude, and the codes at it: rint(v / s) by a
-// multiplication with 1 / s (a division per value costs more than the rest of a code),
-// clamped to +-127; 0 where s is 0 and for a NaN.  Where 1 / s overflows (s below
-// 2^-128), v / s itself.
+// multiplication with 1 / s (a division per value costs more than the rest of a
+// code); 0 where s is 0 and for a NaN.  Where 1 / s overflows (s below 2^-128, a
+// scale of few bits), v / s itself, kept to +-127.
 struct CodeScale {
     float s, inv;
-    __device__ __forceinline__ int code(float v) const {
-        const float q = inv <= 3.402823466e+38f ? __fmul_rn(v, inv) : __fdiv_rn(v, s);
-        return max(-127, min(127, __float2int_rn(q)));
+    // The rounding to an integer is that of an addition: v / s is at most 127 and a
+    // rounding, and 1.5 * 2^23 + q has q, to the nearest even, in its lowest bits (the
+    // converting instruction runs at a quarter of the rate).
+    __device__ __forceinline__ uint32_t code_bits(float v) const {  // the code in the lowest byte
+        const float q = inv <= 3.402823466e+38f ? __fmul_rn(v, inv) : fminf(fmaxf(__fdiv_rn(v, s), -127.0f), 127.0f);
+        return q == q ? __float_as_uint(__fadd_rn(q, 12582912.0f)) : 0u;
     }
+    __device__ __forceinline__ int code(float v) const { return (int8_t)(code_bits(v) & 0xffu); }
     __device__ __forceinline__ uint32_t code4(float4 v) const {
-        return ((uint32_t)code(v.x) & 0xffu) | (((uint32_t)code(v.y) & 0xffu) << 8) |
-               (((uint32_t)code(v.z) & 0xffu) << 16) | (((uint32_t)code(v.w) & 0xffu) << 24);
+        const uint32_t lo = __byte_perm(code_bits(v.x), code_bits(v.y), 0x0040);
+        const uint32_t hi = __byte_perm(code_bits(v.z), code_bits(v.w), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
     }
 };
 __device__ __forceinline__ CodeScale code_scale(float amax) {

@@ -8,6 +8,8 @@
 //   y  = residual_scale * residual + block_scale * gate_t[t] * gate_h[h] * zn
 //   xn = y * rsqrt(mean(y^2) + eps) * (offset + next_w)             (y as stored)
 //   sx = max |xn| / 127,  xq = rint(xn / sx)                        (xn before its rounding)
+#include <cuda_bf16.h>
+
 #include "i8_math.cuh"
 #include "ops.cuh"
 
@@ -27,8 +29,10 @@ __device__ __forceinline__ void unpack8(uint4 u, float v[8]) {
 __device__ __forceinline__ uint4 pack8(const float v[8]) {
     uint32_t p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        p[i] = (uint32_t)f32_to_bf16_rne(v[2 * i]) | ((uint32_t)f32_to_bf16_rne(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        p[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
     return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
@@ -46,8 +50,15 @@ __device__ __forceinline__ float row_reduce(float v, float *s_part) {
     if (nw == 1) return v;
     if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = s_part[0];
-    for (int i = 1; i < nw; ++i) v = MAX ? fmaxf(v, s_part[i]) : v + s_part[i];
+    // four partials a load, added in turn
+    v = MAX ? 0.0f : -0.0f;
+    for (int i = 0; i < nw; i += 4) {
+        const float4 u = *reinterpret_cast<const float4 *>(s_part + i);
+        const float w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < nw) v = MAX ? fmaxf(v, w[j]) : v + w[j];
+    }
     return v;
 }
 
@@ -65,10 +76,10 @@ __device__ __forceinline__ void load8(const float *p, float v[8]) {
 // more rows in flight (fewer registers) hide a row's chain.
 constexpr int kMaxThreads = 512;
 template <int SRC, int CH, bool FEW>
-__global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : (SRC == kSrcRows ? 3 : 2)) k_norm(const NormArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : 2) k_norm(const NormArgs a) {
     constexpr bool EARLY = (FEW || SRC != kSrcRows) && CH <= 2;
-    constexpr int B = FEW ? 8 : 2;  // routes at a time (many rows: 2 at three CTAs an SM, 147 us; 4 at two, 196)
-    __shared__ float s_part[3][32];
+    constexpr int B = FEW ? 8 : 2;  // routes at a time (many rows: 2, 148 us; 1, 157; 3, 176; 4, 188)
+    __shared__ __align__(16) float s_part[3][32];
     pdl_wait();
     pdl_launch_dependents();
     const int t = blockIdx.x * blockDim.y + threadIdx.y, nch = a.H / 8;
@@ -132,7 +143,7 @@ __global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : (SRC == kSrcR
             for (int c = 0; c < CH; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) ss = __fmaf_rn(v[c][i], v[c][i], ss);
-            r = __frsqrt_rn(row_reduce<false>(ss, s_part[0]) / (float)a.H + a.eps);
+            r = __frsqrt_rn(__fmaf_rn(row_reduce<false>(ss, s_part[0]), a.inv_h, a.eps));
         }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -161,7 +172,7 @@ __global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : (SRC == kSrcR
     for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __fmaf_rn(v[c][i], v[c][i], ss);
-    const float r = __frsqrt_rn(row_reduce<false>(ss, s_part[1]) / (float)a.H + a.eps);
+    const float r = __frsqrt_rn(__fmaf_rn(row_reduce<false>(ss, s_part[1]), a.inv_h, a.eps));
     float amax = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -194,8 +205,11 @@ __global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : (SRC == kSrcR
 // 512 threads.  A row's layout, and so the order of its sums, depends on its width
 // alone: a row's result is the same in any batch, and whether the norm before the next
 // block runs here or by itself.
-// Measured: one token of 8 routes 5.8 -> 4.3 us (FEW); 8192 tokens of 8 routes, 2816
-// wide, 157 -> 147 us, 6.0 TB/s of 876 MB.
+// Measured, 2816 wide: one token of 8 routes 3.9 us; 8192 tokens of 8 routes 148 us,
+// 5.9 TB/s of 876 MB; moe_norm alone of 1023 rows 4.0 us (with codes 6.5), of 16384
+// rows 55 us, 3.4 TB/s: there the integer pipe bounds it (unpacking, rounding and packing bf16,
+// the threads' share of the reductions), not HBM; four rows on the same threads, for more
+// loads in flight, were no faster.
 constexpr int kFewRows = 256;
 
 template <int SRC, bool FEW>

@@ -33,6 +33,7 @@ struct NormArgs {
     uint16_t *y, *xn;
     int8_t *xq;
     float *sx;
+    float inv_h;  // 1 / H
 };
 cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t s);
 

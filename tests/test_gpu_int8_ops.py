@@ -567,6 +567,22 @@ def test_run_together_replayed_and_on_other_streams(T):
     no_device_error()
 
 
+def test_norm_codes_of_tiny_rows():
+    """Rows whose scale has few bits left, or none: codes stay in range and stand for the values."""
+    H = 128
+    x = torch.zeros((6, H), dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(DEV).manual_seed(1)
+    for t, size in enumerate([1e-36, 1e-38, 1e-39, 1e-40, 0.0]):
+        x[t] = (size * torch.randn(H, device=DEV, generator=g)).bfloat16()
+    x[5, 3] = 1e-39
+    w = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    out = moe.moe_norm(x, w, eps=1.0, codes=True)  # r = 1: n is x
+    n, q, s = f64(x), f64(out.xq), f64(out.sx)[:, None]
+    assert np.abs(q).max() <= 127
+    # half a code, and what 1 / 127 of a maximum of 2^-149 steps loses in sx (half a step of it a code)
+    assert np.all(np.abs(q * s - n) <= 0.51 * s + 127 * 2.0 ** -150 + 2.0 ** -149)
+
+
 @pytest.mark.parametrize("T", [2, 60])
 def test_calls_on_a_given_stream(T):
     """`stream=`: results as on the current one, with outputs and workspace made by the
