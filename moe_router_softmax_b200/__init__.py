@@ -119,8 +119,7 @@ def _check(st: int) -> None:
 
 def _stream(stream=None):
     # the current stream's raw handle: building a Stream object for it costs 3 us
-    raw = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
-    return ctypes.c_void_p(raw)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
 def _dev(t: torch.Tensor | None, dtype=None, name="tensor"):
@@ -132,7 +131,7 @@ def _dev(t: torch.Tensor | None, dtype=None, name="tensor"):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _host(a: np.ndarray, dtype):
@@ -185,9 +184,9 @@ class MoeLayer:
     def refresh(self):
         """Re-read the tensors' addresses (after replacing pool or slot_table)."""
         self._c.fmt, self._c.E, self._c.H, self._c.I = self.fmt, self.E, self.H, self.I
-        self._c.home = _dev(self.home, torch.uint8, "home").value
-        self._c.pool = None if self.pool is None else _dev(self.pool, torch.uint8, "pool").value
-        self._c.slot_table = None if self.slot_table is None else _dev(self.slot_table, torch.int32, "slot_table").value
+        self._c.home = _dev(self.home, torch.uint8, "home")
+        self._c.pool = None if self.pool is None else _dev(self.pool, torch.uint8, "pool")
+        self._c.slot_table = None if self.slot_table is None else _dev(self.slot_table, torch.int32, "slot_table")
         self._c.expert_bytes = self.expert_bytes
         self._c.pool_slots = self.pool_slots
         return self
