@@ -37,7 +37,6 @@ struct CodeScale {
         const float q = inv <= 3.402823466e+38f ? __fmul_rn(v, inv) : fminf(fmaxf(__fdiv_rn(v, s), -127.0f), 127.0f);
         return q == q ? __float_as_uint(__fadd_rn(q, 12582912.0f)) : 0u;
     }
-    __device__ __forceinline__ int code(float v) const { return (int8_t)(code_bits(v) & 0xffu); }
     __device__ __forceinline__ uint32_t code4(float4 v) const {
         const uint32_t lo = __byte_perm(code_bits(v.x), code_bits(v.y), 0x0040);
         const uint32_t hi = __byte_perm(code_bits(v.z), code_bits(v.w), 0x0040);

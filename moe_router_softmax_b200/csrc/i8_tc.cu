@@ -23,10 +23,10 @@
 // CTAs report to the leader's barriers, its MMA warp issues for both, and its
 // commits free the slots of both.
 //
-// Measured on B200 (device time): linear 4096 x 8192 x 2816 in 67.5 us, 2.80 POP/s (one
+// Measured on B200 (device time): linear 4096 x 8192 x 2816 in 65 us, 2.92 POP/s (one
 // CTA per tile: 79; bound by the tensor pipe and power); FFN of 64 tokens (128 experts,
-// hidden 2816, intermediate 704, top-8), combine included, 116 us, 6.4 TB/s of the active
-// experts; of 2047 tokens 293 us.  Pairs gained the phases nothing (292 to 304 us).
+// hidden 2816, intermediate 704, top-8), combine included, 115 us, 6.5 TB/s of the active
+// experts; of 2047 tokens 283 us.  Pairs gained the phases nothing (287 to 304 us).
 //
 // Persistent CTAs, one per SM; warp 0 TMA producer of the weights, warp 1 TMEM
 // allocation and the MMA issuer, warps 2..9 epilogue (TMEM -> registers ->

@@ -78,7 +78,8 @@ constexpr int kMaxThreads = 512;
 template <int SRC, int CH, bool FEW>
 __global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : 2) k_norm(const NormArgs a) {
     constexpr bool EARLY = (FEW || SRC != kSrcRows) && CH <= 2;
-    constexpr int B = FEW ? 8 : 2;  // routes at a time (many rows: 2, 148 us; 1, 157; 3, 176; 4, 188)
+    // routes at a time (many rows: 2, 148 us; 1, 157; 3, 176; 4, 188)
+    constexpr int B = FEW ? (CH == 1 ? 8 : 4) : 2;
     __shared__ __align__(16) float s_part[3][32];
     pdl_wait();
     pdl_launch_dependents();

@@ -318,6 +318,39 @@ def test_ffn_w8a8_every_token_to_one_expert(T):
     no_device_error()
 
 
+@pytest.mark.parametrize("E,H,I,k,T,skew", [
+    (2, 128, 64, 1, 600, 0.9),       # an expert with more routes than one block holds
+    (3, 192, 128, 2, 700, 0.0),
+    (300, 64, 64, 5, 333, 0.0),      # more experts than lanes or warps
+    (1024, 64, 64, 3, 900, 0.5), (40, 128, 128, 8, 257, 0.7)])
+def test_ffn_w8a8_many_routes(E, H, I, k, T, skew):
+    L, pieces = int8_layer(E, H, I, seed=E)
+    xq, sx = tokens(T, H, seed=5)
+    r = np.random.default_rng([E, T])
+    score = r.standard_normal((T, E))
+    score[r.random(T) < skew, 0] -= 100.0   # that share of the tokens takes expert 0
+    ids = np.argsort(score, axis=1)[:, :k].astype(np.int32)
+    counts, offsets, sr, rp = moe.moe_permute(dev(ids), E)
+    rows = moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(sx), k, counts, offsets, sr)
+    check_ffn(L, pieces, xq, sx, ids, rows, rp)
+    no_device_error()
+
+
+def test_ffn_w8a8_the_same_expert_twice():
+    """A token that names an expert twice has two routes of it, with equal rows."""
+    E, H, I, k = 4, 128, 64, 2
+    L, pieces = int8_layer(E, H, I, seed=8)
+    for T in (1, 300):
+        xq, sx = tokens(T, H, seed=T)
+        ids = np.full((T, k), 2, np.int32)
+        counts, offsets, sr, rp = moe.moe_permute(dev(ids), E)
+        rows = moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(sx), k, counts, offsets, sr)
+        check_ffn(L, pieces, xq, sx, ids, rows, rp, only={0, T - 1})
+        by_route = rows[rp.long()].view(T, k, H)
+        assert torch.equal(by_route[:, 0], by_route[:, 1])
+    no_device_error()
+
+
 @pytest.mark.parametrize("T", [1, 5, 70])
 def test_ffn_w8a8_slot_table(T):
     E, H, I, k = 8, 256, 128, 3
