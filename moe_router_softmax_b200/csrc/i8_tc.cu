@@ -338,7 +338,10 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
     __syncthreads();
     if (CG == 2) cluster_sync();  // the other CTA's barriers are set up
     tc_fence_after();
-    // the next launch may take over SMs as this grid's CTAs finish
+    // The next launch may take over SMs as this grid's CTAs finish.  The dense product
+    // waits for the launch before it first: a later one that reads its own weights ahead
+    // of its wait (the FFN's second phases do) may rely on all that came before this.
+    if (MODE < kPhase1) pdl_wait();
     pdl_launch_dependents();
     const uint32_t tmem = s_tmem;
     const int total = s_items.total, n_act = s_items.n_act;
@@ -389,10 +392,8 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
     if (warp == 0) {
         // -------------------------------------------------- weights
         if (lane == 0) {
-            // The dense product's weights may come from the launch before; the
-            // phases' launches follow this library's own (gather, codes of h),
-            // which have waited for all before them and write no weights.
-            if (MODE < kPhase1) pdl_wait();
+            // (the phases' launches follow this library's own, gather and codes of h,
+            // which have waited for all before them and write no weights)
             const uint64_t pol = MODE < kPhase1 ? l2_policy_normal() : l2_policy_first();
             int st = 0;
             uint32_t ph = 0;
@@ -673,9 +674,9 @@ k_i8_split(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_wait();  // operands and scales may come from the launch before
     pdl_launch_dependents();
     const uint32_t tmem = s_tmem;
-    pdl_wait();  // operands and scales may come from the launch before
 
     if (warp == 0) {
         if (lane == 0) {

@@ -647,6 +647,33 @@ def test_calls_on_a_given_stream(T):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("T", [1, 3, 40, 300])
+def test_operands_rewritten_between_calls(T):
+    """Calls in a row on one stream whose weights and codes the launch before writes."""
+    N, K, n = 300, 1024, 12
+    g = torch.Generator(DEV).manual_seed(T)
+    ws = [torch.randn(N, K, device=DEV, generator=g).bfloat16() for _ in range(2)]
+    xs = [torch.randn(T, K, device=DEV, generator=g).bfloat16() for _ in range(2)]
+    nw = torch.ones(K, dtype=torch.bfloat16, device=DEV)
+    wq, sw = torch.empty((N, K), dtype=torch.int8, device=DEV), torch.empty(N, device=DEV)
+    xq, sx = torch.empty((T, K), dtype=torch.int8, device=DEV), torch.empty(T, device=DEV)
+
+    def step(i, wait):
+        moe.moe_quantize_int8(ws[i % 2], q=wq, scale=sw)
+        if wait:
+            torch.cuda.synchronize()
+        moe.moe_norm(xs[(i // 2) % 2], nw, codes=True, want_xn=False, xq=xq, sx=sx)
+        if wait:
+            torch.cuda.synchronize()
+        return moe.moe_linear_int8(xq, sx, wq, sw)
+
+    want = [step(i, True).clone() for i in range(4)]
+    torch.cuda.synchronize()
+    got = [step(i, False) for i in range(n)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[i], want[i % 4]) for i in range(n))
+
+
 def test_run_together_against_the_formulas():
     """One block, each step held to its reference on the step's own inputs."""
     T, E, H, I, k = 9, 16, 256, 128, 4
