@@ -852,10 +852,15 @@ template <int MODE, int ATOMS, int CG>
 cudaError_t launch_tc(const CUtensorMap &mh, const CUtensorMap &mp, const void *b, const TcI8Params &p, int n_sm,
                       cudaStream_t s) {
     TokenMaps mb;
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+        if (i > 0 && (MODE < kPhase1 || (8 << i) >= p.R)) {  // a box that no block of R rows needs: not read
+            mb.m[i] = mb.m[i - 1];
+            continue;
+        }
         if (!encode_2d(&mb.m[i], b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)p.K, (uint64_t)p.R, kKB,
                        MODE < kPhase1 ? (uint32_t)block_rows<CG>(p.R) / CG : 16u << i, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
+    }
     auto kern = k_i8_tc<MODE, ATOMS, CG>;
     static bool attr[kMaxDevices] = {};
     int dev = 0;
@@ -985,16 +990,19 @@ cudaError_t launch_ffn_i8_tc(const FfnI8Args &a, cudaStream_t s) {
     float *ss = reinterpret_cast<float *>(at);
 
     const bool slotted = a.L.slot_table != nullptr;
-    const uint8_t *pool = slotted ? a.L.pool : a.L.home;
-    const uint64_t slots = slotted ? (uint64_t)a.L.pool_slots : (uint64_t)E;
     CUtensorMap h1, p1, h2, p2;
     if (!encode_w13(&h1, a.L.home + a.L.off.q13, H, I, E, a.L.stride) ||
-        !encode_w13(&p1, pool + a.L.off.q13, H, I, slots, a.L.stride) ||
         !encode_3d(&h2, a.L.home + a.L.off.q2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, I, H, E, a.L.stride, kKB, kM,
-                   CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_3d(&p2, pool + a.L.off.q2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, I, H, slots, a.L.stride, kKB, kM,
                    CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
+    if (!slotted) {
+        p1 = h1;  // not read
+        p2 = h2;
+    } else if (!encode_w13(&p1, a.L.pool + a.L.off.q13, H, I, (uint64_t)a.L.pool_slots, a.L.stride) ||
+               !encode_3d(&p2, a.L.pool + a.L.off.q2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, I, H,
+                          (uint64_t)a.L.pool_slots, a.L.stride, kKB, kM, CU_TENSOR_MAP_SWIZZLE_128B)) {
+        return cudaErrorInvalidValue;
+    }
 
     const int blocks = (int)std::min<int64_t>(((int64_t)R + 7) / 8, (int64_t)n_sm * 8);
     err = launch_pdl(k_gather_i8, dim3((unsigned)blocks), dim3(256), 0, s, a.xq, a.sx, a.sorted_route, a.offsets, E, a.k,
