@@ -349,7 +349,8 @@ MOE_API moe_status moe_linear_int8(const int8_t *xq, const float *sx, const int8
  *   sh = max |h| / 127;  hq = clamp(rint(h / sh), -127, 127)           (per row)
  *   rows[s] = s2 sh (Q2_e hq)
  * with exact integer sums, fp32 elsewhere.  h is quantised from its fp32 value, a
- * scale per row, so that its codes do not depend on a rounding in between.  rows fp32 [T*k][H] in
+ * scale per row, so that its codes do not depend on a rounding in between; where h
+ * holds a NaN (as a token's whose scale is one), sh and the whole row are NaN.  rows fp32 [T*k][H] in
  * sorted order for moe_combine or moe_combine_norm; rows past offsets[E] are not
  * written.  ws: at least moe_grouped_ffn_w8a8_workspace() bytes, 16-byte aligned;
  * calls that overlap on the GPU need a workspace each.  Slot tables as in
@@ -367,8 +368,9 @@ MOE_API moe_status moe_grouped_ffn_w8a8(const moe_layer *layer, const int8_t *xq
  *   xn = n rounded to bf16;   sx = max |n| / 127,  xq = rint(n / sx)   (codes)
  * x bf16 [T][H], weight bf16 [H]; xn bf16 [T][H] and xq int8 [T][H] with sx fp32
  * [T] are outputs, either of the two nullable (xq and sx go together).  The codes
- * are those of n before its rounding to bf16; a row of zeros has scale 0, and a
- * NaN takes no part in the maximum and has code 0.
+ * are those of n before its rounding to bf16; a row of zeros has scale 0, and a row
+ * that holds a NaN or an infinity (whose norm is NaN) scale NaN and codes 0, so that
+ * products of it are NaN.
  *
  * moe_residual_norm and moe_combine_norm are what follows a block: its output z
  * is normalised, gated and added to the residual, and the sum is normalised for

@@ -168,13 +168,13 @@ __global__ void __launch_bounds__(32 * kWarps, 6) k_ffn_i8_gemv2(const FfnI8Args
     float amax = 0.0f;
     for (int i = threadIdx.x; i < I / 4; i += 32 * kWarps) {
         const float4 v = hr[i];
-        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+        amax = max_nan(amax, max_nan(max_nan(fabsf(v.x), fabsf(v.y)), max_nan(fabsf(v.z), fabsf(v.w))));
     }
     amax = warp_max(amax);
     if (lane == 0) s_part[warp] = amax;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) amax = fmaxf(amax, s_part[i]);
+    for (int i = 0; i < kWarps; ++i) amax = max_nan(amax, s_part[i]);
     const CodeScale sc = code_scale(amax);
     for (int i = threadIdx.x; i < I / 4; i += 32 * kWarps) reinterpret_cast<uint32_t *>(s_hq)[i] = sc.code4(hr[i]);
     __syncthreads();

@@ -18,15 +18,22 @@ __device__ __forceinline__ float gate_up(int g_sum, int u_sum, float s_token, fl
     return __fmul_rn(__fmul_rn(__fmul_rn(0.5f, v), __fadd_rn(1.0f, t)), u);
 }
 
+// Maximum of magnitudes that a NaN takes part in (and wins): the codes of a row hold
+// none, so it is the row's scale that has to carry one on.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    for (int off = 16; off > 0; off >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, off));
     return v;
 }
 
 // Scale of a row from its largest magnitude, and the codes at it: rint(v / s) by a
 // multiplication with 1 / s (a division per value costs more than the rest of a
-// code); 0 where s is 0 and for a NaN.  Where 1 / s overflows (s below 2^-128, a
+// code); 0 where s is 0 or NaN and for a NaN.  Where 1 / s overflows (s below 2^-128, a
 // scale of few bits), v / s itself, kept to +-127.
 struct CodeScale {
     float s, inv;
@@ -46,7 +53,7 @@ struct CodeScale {
 __device__ __forceinline__ CodeScale code_scale(float amax) {
     CodeScale c;
     c.s = __fdiv_rn(amax, 127.0f);
-    c.inv = c.s != 0.0f ? __fdiv_rn(1.0f, c.s) : 0.0f;
+    c.inv = c.s > 0.0f ? __fdiv_rn(1.0f, c.s) : 0.0f;
     return c;
 }
 

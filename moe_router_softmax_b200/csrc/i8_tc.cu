@@ -810,7 +810,9 @@ __global__ void __launch_bounds__(256) k_codes_h(const float *__restrict__ h, co
     uint32_t *dst = reinterpret_cast<uint32_t *>(hq + (size_t)s * I);
     float4 v[V > 0 ? V : 1];
     float amax = 0.0f;
-    auto grow = [&](float4 u) { amax = fmaxf(amax, fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w)))); };
+    auto grow = [&](float4 u) {
+        amax = max_nan(amax, max_nan(max_nan(fabsf(u.x), fabsf(u.y)), max_nan(fabsf(u.z), fabsf(u.w))));
+    };
     if (V > 0) {
 #pragma unroll
         for (int i = 0; i < V; ++i)

@@ -44,7 +44,7 @@ __device__ __forceinline__ float row_reduce(float v, float *s_part) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         const float o = __shfl_xor_sync(0xffffffffu, v, off);
-        v = MAX ? fmaxf(v, o) : v + o;
+        v = MAX ? max_nan(v, o) : v + o;
     }
     const int nw = (int)(blockDim.x >> 5);
     if (nw == 1) return v;
@@ -57,7 +57,7 @@ __device__ __forceinline__ float row_reduce(float v, float *s_part) {
         const float w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (i + j < nw) v = MAX ? fmaxf(v, w[j]) : v + w[j];
+            if (i + j < nw) v = MAX ? max_nan(v, w[j]) : v + w[j];
     }
     return v;
 }
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : 2) k_norm(con
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             v[c][i] = __fmul_rn(__fmul_rn(v[c][i], r), __fadd_rn(a.offset, wv[i]));
-            amax = fmaxf(amax, fabsf(v[c][i]));
+            amax = max_nan(amax, fabsf(v[c][i]));
         }
         if (a.xn) reinterpret_cast<uint4 *>(a.xn + base)[ch] = pack8(v[c]);
     }

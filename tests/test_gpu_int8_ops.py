@@ -700,3 +700,44 @@ def test_run_together_against_the_formulas():
     # without its norms and residual the block's end is moe_combine, bit for bit
     plain = moe.moe_combine_norm(rows, rp, w, torch.zeros_like(xt))
     assert torch.equal(plain.y, moe.moe_combine(rows, rp, w))
+
+
+# ------------------------------------------------------------------ NaN and infinities on their way
+
+def test_norm_scale_of_a_row_with_a_nan():
+    """codes of 0 alone would turn the row into zeros: its scale is NaN."""
+    for T, H in ((5, 128), (300, 2816), (5, 8256), (300, 16384)):
+        r = np.random.default_rng([T, H])
+        xt, _ = bf16(r.standard_normal((T, H)))
+        w = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+        clean = moe.moe_norm(xt, w, codes=True)
+        bad = torch.zeros(T, dtype=torch.bool, device=DEV)
+        for t, c, v in ((1, H - 1, float("nan")), (2, 0, float("inf")), (4, H // 2, float("-inf"))):
+            xt[t, c] = v
+            bad[t] = True
+        out = moe.moe_norm(xt, w, codes=True)
+        assert torch.isnan(out.sx[bad]).all() and (out.xq[bad] == 0).all()
+        assert torch.equal(out.sx[~bad], clean.sx[~bad]) and torch.equal(out.xq[~bad], clean.xq[~bad])
+        # and the product of such a row is NaN
+        y = moe.moe_linear_int8(out.xq, out.sx, clean.xq[:5].contiguous(), clean.sx[:5].contiguous())
+        assert torch.isnan(y[bad]).all() and torch.isfinite(y[~bad].float()).all()
+
+
+@pytest.mark.parametrize("T", [2, 6, 70])
+@pytest.mark.parametrize("I", [128, 832])
+def test_ffn_w8a8_token_without_a_number(T, I):
+    E, H, k = 4, 128, 2
+    L, _ = int8_layer(E, H, I, seed=12)
+    xq, sx = tokens(T, H, seed=13)
+    r = np.random.default_rng(T)
+    ids = np.argsort(r.random((T, E)), axis=1)[:, :k].astype(np.int32)
+    counts, offsets, sr, rp = moe.moe_permute(dev(ids), E)
+    clean = moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(sx), k, counts, offsets, sr)
+    for v in (float("nan"), float("inf")):
+        s2 = sx.copy()
+        s2[1] = v
+        rows = moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(s2), k, counts, offsets, sr)
+        bad = torch.zeros(T * k, dtype=torch.bool, device=DEV)
+        bad[rp[k:2 * k].long()] = True
+        assert torch.isnan(rows[bad]).all() and torch.equal(rows[~bad], clean[~bad])
+    no_device_error()
