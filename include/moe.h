@@ -368,7 +368,9 @@ MOE_API moe_status moe_grouped_ffn_w8a8(const moe_layer *layer, const int8_t *xq
  *   xn = n rounded to bf16;   sx = max |n| / 127,  xq = rint(n / sx)   (codes)
  * x bf16 [T][H], weight bf16 [H]; xn bf16 [T][H] and xq int8 [T][H] with sx fp32
  * [T] are outputs, either of the two nullable (xq and sx go together).  The codes
- * are those of n before its rounding to bf16; a row of zeros has scale 0, and a row
+ * are those of n before its rounding to bf16, and n / sx is formed as 127 p / max |p|,
+ * p = x[t] * (offset + weight), in which the row's norm cancels: with offset 0 a code is
+ * the nearest one to the exact quotient, ties to even.  A row of zeros has scale 0, and a row
  * that holds a NaN or an infinity (whose norm is NaN) scale NaN and codes 0, so that
  * products of it are NaN.
  *

@@ -8,6 +8,11 @@
 //   y  = residual_scale * residual + block_scale * gate_t[t] * gate_h[h] * zn
 //   xn = y * rsqrt(mean(y^2) + eps) * (offset + next_w)             (y as stored)
 //   sx = max |xn| / 127,  xq = rint(xn / sx)                        (xn before its rounding)
+// In xn / sx = 127 xn / max |xn| the row's norm cancels, and any factor of it does.  The
+// codes are formed from p = y f (offset + next_w), f = 127 times a power of two: without an
+// offset p is exact (8 bits of y, 7 of 127, 8 of the weight), and so is max |p| / 127, so that a code
+// carries neither the rounding of the sum of squares nor those of xn and sx: it is the
+// definition's, halves included.
 #include <cuda_bf16.h>
 
 #include "i8_math.cuh"
@@ -174,7 +179,25 @@ __global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : 2) k_norm(con
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __fmaf_rn(v[c][i], v[c][i], ss);
     const float r = __frsqrt_rn(__fmaf_rn(row_reduce<false>(ss, s_part[1]), a.inv_h, a.eps));
-    float amax = 0.0f;
+    if (a.xq == nullptr) {  // without codes: xn alone, by the same operations
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int ch = threadIdx.x + c * blockDim.x;
+            if (ch >= nch) continue;
+            if (!EARLY) nw[c] = __ldg(reinterpret_cast<const uint4 *>(a.next_w) + ch);
+            float wv[8];
+            unpack8(nw[c], wv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) wv[i] = __fmul_rn(__fmul_rn(v[c][i], r), __fadd_rn(a.offset, wv[i]));
+            reinterpret_cast<uint4 *>(a.xn + base)[ch] = pack8(wv);
+        }
+        return;
+    }
+    // r = f rr, f = 127/128 of a power of two, 1 <= rr < 2.02: p has the range of n = p rr
+    const uint32_t r_exp = __float_as_uint(r) & 0x7f800000u;
+    const float f = __fmul_rn(__uint_as_float(r_exp), 127.0f / 128.0f);
+    const float rr = __fmul_rn(__fmul_rn(r, __uint_as_float(0x7f000000u - r_exp)), 128.0f / 127.0f);
+    float amax = 0.0f;  // of p
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int ch = threadIdx.x + c * blockDim.x;
@@ -184,14 +207,26 @@ __global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : 2) k_norm(con
         unpack8(nw[c], wv);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[c][i] = __fmul_rn(__fmul_rn(v[c][i], r), __fadd_rn(a.offset, wv[i]));
-            amax = max_nan(amax, fabsf(v[c][i]));
+            const float w = __fadd_rn(a.offset, wv[i]);
+            wv[i] = __fmul_rn(__fmul_rn(v[c][i], r), w);
+            v[c][i] = __fmul_rn(__fmul_rn(v[c][i], f), w);
         }
-        if (a.xn) reinterpret_cast<uint4 *>(a.xn + base)[ch] = pack8(v[c]);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) amax = max_nan(amax, fabsf(v[c][i]), fabsf(v[c][i + 1]));
+        if (a.xn) reinterpret_cast<uint4 *>(a.xn + base)[ch] = pack8(wv);
     }
-    if (a.xq == nullptr) return;
-    const CodeScale sc = code_scale(row_reduce<true>(amax, s_part[2]));
-    if (threadIdx.x == 0) a.sx[t] = sc.s;
+    amax = row_reduce<true>(amax, s_part[2]);
+    CodeScale sc = code_scale(amax);
+    float sx = __fmul_rn(sc.s, rr);
+    if (sx < 0x1p-126f) {  // a subnormal scale has few bits: the codes are those of n at it
+        sc = code_scale(__fmul_rn(amax, rr));
+        sx = sc.s;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] = __fmul_rn(v[c][i], rr);
+    }
+    if (threadIdx.x == 0) a.sx[t] = sx;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int ch = threadIdx.x + c * blockDim.x;

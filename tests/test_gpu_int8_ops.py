@@ -741,3 +741,88 @@ def test_ffn_w8a8_token_without_a_number(T, I):
         bad[rp[k:2 * k].long()] = True
         assert torch.isnan(rows[bad]).all() and torch.equal(rows[~bad], clean[~bad])
     no_device_error()
+
+
+# ------------------------------------------------------------------ codes next to a half
+
+def exact_codes(x, w):
+    """Codes of the norm of rows x (bf16 values, offset 0): n / sx = 127 x w / max |x w|, in which the row's norm
+    cancels.  A product of two bf16 values has 16 bits, so fp64 holds the quotient to far more than the 2^-25 by which
+    one that is no half differs from it, and a half exactly."""
+    p = x * w
+    return np.rint(127.0 * p / np.abs(p).max(1, keepdims=True))
+
+
+@pytest.mark.parametrize("T,H", [(1, 64), (5, 2816), (300, 1024), (1023, 2816), (2, 8256), (258, 16384)])
+def test_norm_codes_are_the_nearest(T, H):
+    r = np.random.default_rng([T, H])
+    wt, wv = bf16(1.0 + 0.3 * r.standard_normal(H))
+    xt, xv = bf16(r.standard_normal((T, H)) * np.exp(r.standard_normal((T, 1))))
+    out = moe.moe_norm(xt, wt, codes=True)
+    assert np.array_equal(f64(out.xq), exact_codes(xv, wv))
+    # ties: whole numbers under a maximum of 254, every odd one of them a half of a code
+    one, ov = bf16(np.ones(H))
+    v = r.integers(-253, 254, (T, H)).astype(np.float64)
+    v[:, 5] = 254.0
+    xt, xv = bf16(v)
+    assert np.array_equal(f64(moe.moe_norm(xt, one, codes=True).xq), exact_codes(xv, ov))
+    # behind a block
+    z, _ = bf16(r.standard_normal((T, H)))
+    res, _ = bf16(r.standard_normal((T, H)))
+    out = moe.moe_residual_norm(z, res, wt, next_weight=wt, codes=True, want_xn=False)
+    assert np.array_equal(f64(out.xq), exact_codes(f64(out.y), wv))
+    k = 3
+    rows, pos = dev(r.standard_normal((T * k, H)).astype(np.float32)), dev(r.permutation(T * k).astype(np.int32))
+    out = moe.moe_combine_norm(rows, pos, dev(r.random((T, k)).astype(np.float32)), res, next_weight=wt, codes=True)
+    assert np.array_equal(f64(out.xq), exact_codes(f64(out.y), wv))
+
+
+@pytest.mark.parametrize("lo,hi", [(120.0, 127.9), (-120.0, -100.0), (-60.0, 60.0)])
+def test_norm_codes_of_large_and_small_weights(lo, hi):
+    """Weights whose products with a row leave little room below the largest fp32 number, or above the least."""
+    H = 128
+    r = np.random.default_rng(2)
+    wt, wv = bf16(np.exp2(hi - np.minimum(8.0, hi - lo) * r.random(H)))
+    xt, xv = bf16(np.where(r.random((3, H)) < 0.5, -1.0, 1.0))
+    out = moe.moe_norm(xt, wt, codes=True)
+    assert np.array_equal(f64(out.xq), exact_codes(xv, wv))
+    # rsqrt (the 64-bit reference's own square root included) and two products, then a division
+    n, rel = ref.norm(xv, wv, 1e-6, 0.0)
+    assert np.all(np.abs(f64(out.sx) - np.abs(n).max(1) / 127.0) <= (rel + 2 * ref.U32) * np.abs(n).max(1) / 127.0)
+
+
+@pytest.mark.parametrize("T", [1, 3, 70])
+@pytest.mark.parametrize("I", [64, 832])
+def test_ffn_w8a8_codes_next_to_a_half(T, I):
+    """Rows of h that are whole numbers (the gate is large, so gelu is the identity) under scales that are odd whole
+    numbers, every value a half of a code; the second product writes the codes out."""
+    E, H, k = 2, 64, 1
+    r = np.random.default_rng([T, I])
+    for s in (7, 11, 23):
+        # h_i = 16 u_i with max u = 254 s: sh = 32 s, h / sh = u / (2 s)
+        u = s * r.integers(-253, 254, I)
+        u[0] = 254 * s
+        q13 = np.zeros((E, 2 * I, H), np.int8)
+        q13[:, :I, 0] = 16
+        left = u.copy()
+        for j in range(H):
+            q13[:, I:, j] = np.clip(left, -127, 127)
+            left = left - np.clip(left, -127, 127)
+        assert not left.any()
+        q2 = np.zeros((E, H, I), np.int8)
+        cols = r.permutation(I)[:H]
+        cols[0] = 0
+        q2[:, np.arange(H), cols] = 1
+        one = lambda *sh: np.ones(sh, np.float32)  # noqa: E731
+        eb = (moe.moe_expert_bytes(moe.MOE_W_INT8, H, I) + 255) // 256 * 256
+        blob = np.concatenate([v.view(np.uint8).ravel() for v in (q13[0], one(2 * I), q2[0], one(H))])
+        home = np.zeros((E, eb), np.uint8)
+        home[:, :blob.size] = blob
+        L = moe.MoeLayer(moe.MOE_W_INT8, E, H, I, dev(home.ravel()), expert_bytes=eb)
+        xq = np.ones((T, H), np.int8)
+        ids = dev(r.integers(0, E, (T, k)).astype(np.int32))
+        counts, offsets, sr, rp = moe.moe_permute(ids, E)
+        rows = moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(np.ones(T, np.float32)), k, counts, offsets, sr)
+        want = np.rint(u[cols] / (2.0 * s)) * (32.0 * s)  # whole numbers below 2^24: exact in fp32
+        assert np.array_equal(f64(rows), np.broadcast_to(want, (T, H)))
+    no_device_error()
