@@ -826,3 +826,42 @@ def test_ffn_w8a8_codes_next_to_a_half(T, I):
         want = np.rint(u[cols] / (2.0 * s)) * (32.0 * s)  # whole numbers below 2^24: exact in fp32
         assert np.array_equal(f64(rows), np.broadcast_to(want, (T, H)))
     no_device_error()
+
+
+# ------------------------------------------------------------------ sizes past the repository's own shape
+
+@pytest.mark.parametrize("E,H,I,k", [(3, 128, 832, 2), (3, 3136, 64, 2), (2, 4096, 2048, 1), (2, 64, 16384, 1),
+                                     (2, 16384, 64, 2)])
+@pytest.mark.parametrize("T", [1, 7, 20, 45, 90])
+def test_ffn_w8a8_long_rows(E, H, I, k, T):
+    """Rows of h that no warp holds in registers, weight rows that take a second round of loads."""
+    L, pieces = int8_layer(E, H, I, seed=E + H + I)
+    xq, sx = tokens(T, H, seed=k)
+    r = np.random.default_rng([T, H, I])
+    ids = np.argsort(r.standard_normal((T, E)), axis=1)[:, :k].astype(np.int32)
+    counts, offsets, sr, rp = moe.moe_permute(dev(ids), E)
+    rows = moe.moe_grouped_ffn_w8a8(L, dev(xq), dev(sx), k, counts, offsets, sr)
+    check_ffn(L, pieces, xq, sx, ids, rows, rp, only={0, T // 2, T - 1})
+    no_device_error()
+
+
+@pytest.mark.parametrize("T", [3, 4, 113, 128])
+@pytest.mark.parametrize("N,K", [(1, 16), (7, 64), (33, 80), (130, 272), (300, 1040), (64, 2816), (129, 528),
+                                 (1409, 2816), (5000, 1040)])
+def test_linear_int8_block_sizes(T, N, K):
+    """The dp4a product of four tokens, and the largest blocks of the split product."""
+    test_linear_int8(T, N, K)
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_linear_int8_inside_a_buffer(T):
+    N, K = 37, 96
+    r = np.random.default_rng(T)
+    xq, wq = random_codes(r, T, K), random_codes(r, N, K)
+    sx, sw = (0.5 + r.random(T)).astype(np.float32), (0.5 + r.random(N)).astype(np.float32)
+    buf = torch.full(((T * N + 15) // 8 * 8 + 64,), 7.0, device=DEV)
+    y = buf[32:32 + T * N].view(T, N)
+    moe.moe_linear_int8(dev(xq), dev(sx), dev(wq), dev(sw), y=y)
+    want = ref.linear(xq, sx, wq, sw)
+    assert np.all(np.abs(f64(y) - want) <= 3 * (1 + 1e-6) * ref.U32 * np.abs(want))
+    assert (buf[:32] == 7).all() and (buf[32 + T * N:] == 7).all()
