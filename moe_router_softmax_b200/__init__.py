@@ -625,8 +625,10 @@ def moe_grouped_ffn_w8a8(layer: MoeLayer, xq: torch.Tensor, sx: torch.Tensor, k:
     scales sx [T], as moe_norm or moe_quantize_int8 make them): fp32 rows
     [T*k, H] in sorted order, for moe_combine or moe_combine_norm."""
     dev = _device_of(xq, 2, "xq")
-    if layer.home.get_device() != dev:
-        raise ValueError(f"the layer is on {layer.home.device}, xq on {xq.device}")
+    for name in ("home", "pool", "slot_table"):
+        t = getattr(layer, name)
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"the layer's {name} is on {t.device}, xq on {xq.device}")
     T, R = xq.shape[0], xq.shape[0] * k
     rows, p_rows = _out(rows, (R, layer.H), (layer.H, 1), torch.float32, "rows", dev, xq.device, stream)
     if ws is None:

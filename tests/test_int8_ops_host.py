@@ -155,3 +155,29 @@ def test_binding_refuses_host_tensors():
         moe.moe_route_scored(torch.zeros((2, 8)), 2)
     with pytest.raises(ValueError, match="CUDA"):
         moe.moe_linear_int8(x.to(torch.int8), x[:, 0].float(), x.to(torch.int8), x[:, 0].float())
+
+
+class _On:
+    """Stands for a CUDA tensor on a device; its memory is never reached."""
+
+    is_cuda, dtype = True, torch.int8
+
+    def __init__(self, dev, *shape):
+        self.dev, self.shape, self.device = dev, shape, f"cuda:{dev}"
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return self.dev
+
+
+@pytest.mark.parametrize("name", ["home", "pool", "slot_table"])
+def test_ffn_refuses_a_layer_on_another_device(name):
+    class Layer:
+        E, H, I = 4, 64, 64
+        home, pool, slot_table = _On(0), _On(0), _On(0)
+
+    setattr(Layer, name, _On(1))
+    with pytest.raises(ValueError, match=f"{name} is on cuda:1"):
+        moe.moe_grouped_ffn_w8a8(Layer(), _On(0, 2, 64), None, 2, None, None, None)
