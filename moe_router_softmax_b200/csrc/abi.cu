@@ -428,7 +428,7 @@ moe_status moe_linear_int8(const int8_t *xq, const float *sx, const int8_t *wq, 
 
 size_t moe_grouped_ffn_w8a8_workspace(const moe_layer *layer, int32_t T, int32_t k) {
     if (!layer || T < 0 || k < 1) return 0;
-    return align256(ffn_i8_workspace(layer->H, layer->I, T, k));
+    return align256(ffn_i8_workspace(layer->E, layer->H, layer->I, T, k));
 }
 
 moe_status moe_grouped_ffn_w8a8(const moe_layer *layer, const int8_t *xq, const float *sx, int32_t T, int32_t k,
@@ -444,7 +444,7 @@ moe_status moe_grouped_ffn_w8a8(const moe_layer *layer, const int8_t *xq, const 
     if (T == 0) return MOE_OK;
     CHECK_ARG(xq && sx && counts && offsets && sorted_route && rows && ws, "moe_grouped_ffn_w8a8: NULL pointer");
     CHECK_ARG(aligned16(xq) && aligned16(rows) && aligned16(ws), "xq, rows and ws must be 16-byte aligned");
-    const size_t need = align256(ffn_i8_workspace(v.H, v.I, T, k));
+    const size_t need = align256(ffn_i8_workspace(v.E, v.H, v.I, T, k));
     CHECK_ARG(ws_bytes >= need, "workspace %zu bytes < %zu needed", ws_bytes, need);
     const FfnI8Args a{v, xq, sx, T, k, counts, offsets, sorted_route, rows, ws};
     return cuda_status(launch_ffn_i8(a, (cudaStream_t)stream), "moe_grouped_ffn_w8a8 launch");

@@ -8,6 +8,10 @@
 //
 // A weight row is read once, 16 bytes per lane, so the weights' bytes bound
 // these kernels.
+#include <math.h>
+
+#include <algorithm>
+
 #include "i8_math.cuh"
 #include "ops.cuh"
 
@@ -21,11 +25,20 @@ constexpr int kWarps = 4;
 //   linear: 2816 x 2816, 2 tokens 4.4 / 5.2 us, 4 tokens 6.9 / 5.2; 8192 x 2816, 2
 //   tokens 7.7 / 9.4, 4 tokens 12.8 / 9.4; 1408 x 704, 4 tokens 3.5 / 4.8 (every warp
 //   reads the tokens' codes again, from L1)
-//   ffn (top-8, 128 experts of 2816 x 704): 40 routes 46.4 / 50.3, 48 routes 53.4 / 52.0
+//   ffn: these kernels read an expert's weights once for every route of it, those once,
+//   behind two more launches.  What counts is the bytes that are read again (routes less the
+//   distinct experts of a uniform choice, times 3 H I):
+//     128 experts of 2816 x 704, top-8   40 routes, 28 MB again: 47.0 / 49.0 us; 48, 42 MB: 53.6 / 56.7; 96: 93 / 79
+//     64 of 2048 x 1024, top-6           30, 32 MB: 42.4 / 43.3; 36, 47 MB: 47.2 / 43.8
+//     8 of 1024 x 512, top-2             24, 26 MB: 12.2 / 15.2; 32, 38 MB: 16.4 / 15.2
+//     4 of 4096 x 2048, top-2            8, 128 MB: 38 / 28; 40, 906 MB: 133 / 31
+//     2 of 4096 x 4096, top-1            8, 303 MB: 70 / 32; 40, 1.9 GB: 268 / 35
+//   and, for small experts, the routes (16 of 512 x 256, top-4: 40 routes 9.7 / 14.0, 96 routes 18.8 / 14.1).
 constexpr int kGemvTokens = 2;
 constexpr int kGemvTokensSmall = 4;
 constexpr int64_t kGemvProducts = 20000000;  // T N K, past kGemvTokens
 constexpr int kGemvRoutes = 40;
+constexpr double kGemvAgainBytes = 35e6;
 
 // First problem a kernel of this file recorded (0 = none), read and cleared by
 // moe_take_device_errors(): 0x2005 a slot past the pool, 0x2007 a route out of range.
@@ -211,14 +224,23 @@ cudaError_t launch_linear_i8(const LinearArgs &a, cudaStream_t s) {
     return a.fp32 ? go(k_linear_i8<4, true>) : go(k_linear_i8<4, false>);
 }
 
-size_t ffn_i8_workspace(int H, int I, int T, int k) {
-    return (int64_t)T * k <= kGemvRoutes ? (size_t)T * k * I * 4 : ffn_i8_tc_workspace(H, I, T, k);
+// Whether the kernels of this file take the FFN (by sizes alone: the workspace is asked
+// for before the routes are known; with more tokens it turns false once).
+static bool ffn_i8_gemv(int E, int H, int I, int T, int k) {
+    const double R = (double)T * k;
+    if (R > kGemvRoutes) return false;
+    const double distinct = E * (1.0 - pow(1.0 - (double)std::min(k, E) / E, T));
+    return (R - distinct) * 3.0 * H * I <= kGemvAgainBytes;
+}
+
+size_t ffn_i8_workspace(int E, int H, int I, int T, int k) {
+    return ffn_i8_gemv(E, H, I, T, k) ? (size_t)T * k * I * 4 : ffn_i8_tc_workspace(H, I, T, k);
 }
 
 cudaError_t launch_ffn_i8(const FfnI8Args &a, cudaStream_t s) {
     const int64_t R = (int64_t)a.T * a.k;
     if (R == 0) return cudaSuccess;
-    if (R > kGemvRoutes) return launch_ffn_i8_tc(a, s);
+    if (!ffn_i8_gemv(a.L.E, a.L.H, a.L.I, a.T, a.k)) return launch_ffn_i8_tc(a, s);
     float *h = static_cast<float *>(a.ws);
     const int64_t b1 = R * (a.L.I / kWarps), b2 = R * (a.L.H / kRows2);
     if (b1 > INT32_MAX || b2 > INT32_MAX) return cudaErrorInvalidValue;

@@ -58,7 +58,7 @@ struct FfnI8Args {
     float *rows;       // [T k][H], sorted order
     void *ws;
 };
-size_t ffn_i8_workspace(int H, int I, int T, int k);  // of whichever kernels take the call
+size_t ffn_i8_workspace(int E, int H, int I, int T, int k);  // of whichever kernels take the call
 cudaError_t launch_ffn_i8(const FfnI8Args &a, cudaStream_t s);
 size_t ffn_i8_tc_workspace(int H, int I, int T, int k);
 cudaError_t launch_ffn_i8_tc(const FfnI8Args &a, cudaStream_t s);

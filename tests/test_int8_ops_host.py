@@ -181,3 +181,18 @@ def test_ffn_refuses_a_layer_on_another_device(name):
     setattr(Layer, name, _On(1))
     with pytest.raises(ValueError, match=f"{name} is on cuda:1"):
         moe.moe_grouped_ffn_w8a8(Layer(), _On(0, 2, 64), None, 2, None, None, None)
+
+
+@pytest.mark.parametrize("E,H,I,k,T,rows", [
+    (128, 2816, 704, 8, 1, True), (128, 2816, 704, 8, 5, True), (128, 2816, 704, 8, 6, False),
+    (2, 4096, 4096, 1, 1, True), (2, 4096, 4096, 1, 8, False), (2, 4096, 4096, 1, 40, False),
+    (4, 4096, 2048, 2, 1, True), (4, 4096, 2048, 2, 4, False), (8, 16384, 16384, 8, 1, True),
+    (8, 1024, 512, 2, 8, True), (16, 512, 256, 4, 10, True), (16, 512, 256, 4, 11, False)])
+def test_ffn_few_routes_of_few_large_experts(E, H, I, k, T, rows):
+    """Few routes read an expert's weights once per route, which pays while routes that share an expert add few bytes:
+    the workspace is then the rows of h alone."""
+    need = moe._lib.moe_grouped_ffn_w8a8_workspace(_null_layer(fmt=moe.MOE_W_INT8, E=E, H=H, I=I), T, k)
+    h = (T * k * I * 4 + 255) // 256 * 256
+    assert need == h if rows else need > h
+    # a workspace for more tokens serves fewer
+    assert need >= moe._lib.moe_grouped_ffn_w8a8_workspace(_null_layer(fmt=moe.MOE_W_INT8, E=E, H=H, I=I), T - 1, k)
