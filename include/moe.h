@@ -332,8 +332,8 @@ MOE_API moe_status moe_combine(const float *rows, const int32_t *route_pos, cons
  * xq int8 [T][K], sx fp32 [T] (a token's codes: moe_norm, or moe_quantize_int8 of
  * its row); wq int8 [N][K], sw fp32 [N] (moe_quantize_int8 of the weight); y bf16
  * [T][N], or fp32 [T][N] with out_fp32 != 0.  The sum is exact (int32; codes may
- * be -128), so a result carries the rounding of the scales' products and of its own type
- * only, and it is the same whatever kernel a shape takes.  K a multiple of 16 in [16, 65536]; N >= 1;
+ * be -128), so a result carries its rounding to fp32, those of the two products with the
+ * scales (sx first) and that of its own type, and it is the same whatever kernel a shape takes.  K a multiple of 16 in [16, 65536]; N >= 1;
  * xq, wq and y 16-byte aligned.
  */
 MOE_API moe_status moe_linear_int8(const int8_t *xq, const float *sx, const int8_t *wq, const float *sw, int32_t T,

@@ -6,8 +6,8 @@
 //   ffn     g = s13 sx (Q13 xq);  h_i = gelu_tanh(g_i) g_{I+i}   (fp32)
 //           sh = max |h| / 127,  hq = rint(h / sh);  rows = s2 sh (Q2 hq)
 //
-// A weight row is read once, 16 bytes per lane, so the weights' bytes bound
-// these kernels.
+// A weight row is read once (by the FFN once per route), 16 bytes per lane, so the weights'
+// bytes bound these kernels.
 #include <math.h>
 
 #include <algorithm>

@@ -25,8 +25,8 @@
 //
 // Measured on B200 (device time): linear 4096 x 8192 x 2816 in 65 us, 2.92 POP/s (one
 // CTA per tile: 79; bound by the tensor pipe and power); FFN of 64 tokens (128 experts,
-// hidden 2816, intermediate 704, top-8), combine included, 115 us, 6.5 TB/s of the active
-// experts; of 2047 tokens 283 us.  Pairs gained the phases nothing (287 to 304 us).
+// hidden 2816, intermediate 704, top-8; 107 experts with routes), combine included, 115 us, 5.5 TB/s of those
+// experts' weights; of 2047 tokens 283 us.  Pairs gained the phases nothing (287 to 304 us).
 //
 // Persistent CTAs, one per SM; warp 0 TMA producer of the weights, warp 1 TMEM
 // allocation and the MMA issuer, warps 2..9 epilogue (TMEM -> registers ->
@@ -189,11 +189,11 @@ struct Items {
 };
 
 // Slots of the two rings for token blocks of `rows` rows and stages of ATOMS atoms
-// of K.  Every role pays a few hundred cycles of waits and commits a stage, while an
+// of K.  Every role waits and signals once a stage, while an
 // SM's share of HBM brings a weight atom in ~700 cycles.  So the phases take two atoms
 // at a time where experts hold few routes (FFN of 64 tokens 120 -> 116 us); with many,
-// the weights in flight count for more than the waits (2047 tokens: two atoms 315 us,
-// one 296), and three token slots leave them the rest of the memory.  The dense
+// two atoms were slower (2047 tokens: 315 us, one 296), as they leave fewer stages in
+// flight, and three token slots leave the weights the rest of the memory.  The dense
 // product's operands both come from L2 and get the same number of slots.
 template <int MODE, int ATOMS, int CG>
 __device__ __forceinline__ void split_ring(int rows, Items *it) {

@@ -241,11 +241,13 @@ __global__ void __launch_bounds__(kMaxThreads, FEW || CH > 1 ? 1 : 2) k_norm(con
 // 512 threads.  A row's layout, and so the order of its sums, depends on its width
 // alone: a row's result is the same in any batch, and whether the norm before the next
 // block runs here or by itself.
-// Measured, 2816 wide: one token of 8 routes 3.9 us; 8192 tokens of 8 routes 148 us,
-// 5.9 TB/s of 876 MB; moe_norm alone of 1023 rows 4.0 us (with codes 6.5), of 16384
-// rows 55 us, 3.4 TB/s: there the integer pipe bounds it (unpacking, rounding and packing bf16,
-// the threads' share of the reductions), not HBM; four rows on the same threads, for more
-// loads in flight, were no faster.
+// Measured, 2816 wide: one token of 8 routes 3.7 us (with codes 4.4); 8192 tokens of 8 routes
+// 146 us, 6.0 TB/s of 876 MB; a dense block's 8192 tokens 52 us (71), 3.6 TB/s; moe_norm of
+// 1023 rows 4.7 us (7.5), of 16384 rows 53 us (85), 3.5 TB/s.  Without the routes' loads HBM
+// does not bound it: the schedulers issue in 67% of the cycles (78% with codes), 27 (52)
+// instructions a value for unpacking, rounding and packing and a thread's share of the
+// reductions; for the rest of the cycles the four CTAs that an SM holds, a row each, wait for their
+// loads and barriers.  Four rows on the same threads, for more loads in flight, were no faster.
 constexpr int kFewRows = 256;
 
 template <int SRC, bool FEW>

@@ -11,19 +11,27 @@
 // Which expert wins is decided on scores of 64 bits: c is a sum of a score and
 // a bias, and over a prefill chunk's millions of scores a few pairs at the k-th
 // place are closer than fp32 rounding, where an id would depend on the order of
-// operations.  Nearly every token is decided in fp32 all the same: its choices and
-// group scores are formed in fp32 with a bound on their error, and where every
-// gap that the result rests on (between consecutive winners, between the last one
-// and the next, between the last kept group and the next) exceeds the two errors,
-// 64 bits would decide alike.  Elsewhere, a token or two in a hundred, the candidates
+// operations.  Choices and group scores are formed in fp32 first, with a bound on their
+// error, and where every gap that the result rests on (between consecutive winners,
+// between the last one and the next, between the last kept group and the next) exceeds the
+// two errors, 64 bits would decide alike.  Elsewhere the candidates
 // are put in order in 64 bits: the experts that no gap separates from the k-th, one
 // to a lane, or the groups; where more than 32 are that close, the whole token.  The
 // winners' weights are always formed in 64 bits.
 //
-// Bound by the integer pipe and, in a small batch, by the chain of reductions: 8192
-// tokens of 256 experts in 8 groups read 8.4 MB (1.3 us of HBM), and a token takes some
-// 1000 warp instructions.  Measured on B200, 64 bits throughout -> this: one token 5.5
-// -> 3.4 us, 61 tokens of 165 experts 7.9 -> 6.5, 8192 tokens 23.7 -> 15.3.
+// How many tokens leave the fp32 decision depends on how far apart the k best choices lie
+// (counted over normal logits, without groups): 1 to 3 in a hundred at k = 8, up to
+// 512 experts and logits of spread 1.5 to 2, softmax or sigmoid; but 71 (10 of them as a whole)
+// at 1024 experts and k = 32, whose softmax scores are small beside a bound that does not shrink with
+// them, and 64 to 97 where sigmoid scores saturate (spread 5, 128 to 256 experts, no bias).
+//
+// Bound by latency: 8192 tokens of 256 experts in 8 groups read 8.4 MB (1.3 us of HBM) and
+// take some 1100 warp instructions each, issued in 53% of the cycles (integer pipe 44%) from the 28
+// warps that 68 registers leave room for, each a chain of reductions and votes and then the
+// winners' exponentials and divisions in 64 bits; a small batch is one such chain.  Measured on
+// B200, 64 bits throughout -> this: one token 5.5 -> 3.4 us, 61 tokens of 165 experts 7.9 ->
+// 6.5, 8192 tokens 23.7 -> 15.3.  Without groups: 8192 tokens of 256 experts 10.4 us (sigmoid
+// scores of spread 5, in 64 bits: 12.9), of 1024 experts with k = 8 44 us, with k = 32 182 us.
 #include <math.h>
 
 #include "ops.cuh"
@@ -201,7 +209,8 @@ __device__ __noinline__ int route_exact(const ScoredArgs &a, const float *row, f
 //   sigmoid  s (1 - s) (2 + 1.2 |l|) + 0.5 s + 2 s units, below 2^-21
 //   softmax  s times its exponential's error, weighed by it (2 units), the sum's (a
 //            mean of such errors, 4, and up to 37 roundings) and the division's: below
-//            28 units, 2^-18.2
+//            28 units of s; taken at s = 1 for every score, 2^-18.2, so that small scores
+//            near one another go to 64 bits more often than they have to
 // Adding the bias rounds by half a unit of c, and a key gives up the bits that hold
 // its slot (below VPL units).  Two choices whose gap exceeds twice the sum of both errors
 // stand in the same order in 64 bits.  size: |c| + |d|, and for group scores, sums of
@@ -223,8 +232,8 @@ __device__ __forceinline__ float choice32(uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 
-// Lane l holds experts l V .. l V + V-1, V = ceil(E / 32) <= VPL.  The integer pipe
-// (compares, selects, minima) bounds a prefill batch, so a key holds its slot in its
+// Lane l holds experts l V .. l V + V-1, V = ceil(E / 32) <= VPL.  Compares, selects and
+// minima are most of a token's instructions, so a key holds its slot in its
 // lowest bits: the best of a lane is VPL - 1 maxima, the warp's best one reduction and
 // one vote, and equal choices, which this order would get wrong, are never far apart.
 template <int VPL>
