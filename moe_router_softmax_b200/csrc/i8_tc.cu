@@ -469,11 +469,13 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         // The whole warp walks the stages and an elected lane issues, so that the
         // descriptors stay in uniform registers.  A wait on a completed phase costs
         // ~130 cycles: the next stage's is tested before this one's products are issued.
+        // (After an abort the waits fail and end the role, for all lanes alike; a look at the
+        // flag of each lane's own might part them.  The epilogue's likewise.)
         int sa = 0, sb = 0, acc = 0;
         uint32_t pa = 0, pb = 0, aph = 0;
         bool ra = false, rb = false;
         const uint64_t desc_a = sw128_desc(smem_u32(ring)), desc_b = sw128_desc(smem_u32(ringb));
-        for (int item = blockIdx.x / CG; rank == 0 && item < total && !s_abort; item += gridDim.x / CG) {
+        for (int item = blockIdx.x / CG; rank == 0 && item < total; item += gridDim.x / CG) {
             const ItemInfo it = decode(item);
             if (!__all_sync(kAll, mbar_wait(&tempty[acc], aph ^ 1, &s_abort))) break;
             tc_fence_after();
@@ -528,7 +530,7 @@ k_i8_tc(const __grid_constant__ CUtensorMap map_home, const __grid_constant__ CU
         uint32_t aph = 0;
         const uint64_t h_pol = l2_policy_last();  // the next launch reads h
         pdl_wait();  // the token rows' scales come from the launch before
-        for (int item = blockIdx.x / CG; item < total && !s_abort; item += gridDim.x / CG) {
+        for (int item = blockIdx.x / CG; item < total; item += gridDim.x / CG) {
             const ItemInfo it = decode(item);
             // output row of this thread, and its scale(s)
             const int m = (it.mt * CG + rank) * kRows + (MODE == kPhase1 ? q * 16 + (lane & 15) : q * 32 + lane);
