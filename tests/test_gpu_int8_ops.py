@@ -865,3 +865,65 @@ def test_linear_int8_inside_a_buffer(T):
     want = ref.linear(xq, sx, wq, sw)
     assert np.all(np.abs(f64(y) - want) <= 3 * (1 + 1e-6) * ref.U32 * np.abs(want))
     assert (buf[:32] == 7).all() and (buf[32 + T * N:] == 7).all()
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def test_linear_int8_offsets_past_32_bits():
+    g = torch.Generator(DEV).manual_seed(5)
+    code = lambda *s: torch.randint(-127, 128, s, generator=g, dtype=torch.int8, device=DEV)  # noqa: E731
+    # a weight of 4.6 GB, by each of the kernels for few tokens
+    N, K = 70001, 65536
+    wq, sw = code(N, K), torch.ones(N, device=DEV)
+    for T in (2, 5):
+        xq = code(T, K)
+        y = moe.moe_linear_int8(xq, torch.ones(T, device=DEV), wq, sw, dtype=torch.float32)
+        for n in (0, 32767, 32768, 65535, 65536, N - 1):  # 32768 and 65536 start at 2^31 and 2^32 bytes
+            want = (xq.double() * wq[n].double()).sum(1)
+            assert bool(((y[:, n].double() - want).abs() <= ref.U32 * want.abs()).all())
+    del wq, y
+    # an output of 2.5e9 values
+    T, N, K = 50001, 50003, 64
+    xq, wq = code(T, K), code(N, K)
+    y = moe.moe_linear_int8(xq, torch.ones(T, device=DEV), wq, torch.ones(N, device=DEV), dtype=torch.float32)
+    for t in (0, 21473, 42947, 42949, 42950, T - 1):  # (rows around 2^30, 2^31 values and the end)
+        assert torch.equal(y[t].double(), wq.double() @ xq[t].double())  # sums below 2^24
+    no_device_error()
+
+
+def test_norm_offsets_past_32_bits():
+    T, H = 140001, 16384
+    w = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    x = torch.randn((64, H), device=DEV, generator=torch.Generator(DEV).manual_seed(6)).bfloat16()
+    x = x.repeat((T + 63) // 64, 1)[:T]
+    out = moe.moe_norm(x, w, codes=True)
+    for lo in (0, 65472, 131072, T - 64):
+        part = moe.moe_norm(x[lo:lo + 64], w, codes=True)
+        for a, b in ((out.xn, part.xn), (out.xq, part.xq), (out.sx, part.sx)):
+            assert torch.equal(a[lo:lo + 64], b)
+
+
+def test_route_scored_offsets_past_32_bits():
+    T, E, k = 4200001, 1024, 1
+    lg = torch.zeros((T, E), device=DEV)
+    at = torch.arange(T, device=DEV)
+    lg[at, at % E] = 3.0
+    ids, _ = moe.moe_route_scored(lg, k)
+    assert torch.equal(ids[:, 0].long(), at % E)
+
+
+def test_ffn_w8a8_offsets_past_32_bits():
+    """Rows of 5.4 GB; routes of one token's codes, so that every expert's rows are alike."""
+    E, H, I, k = 3, 16384, 64, 1
+    T = 82001
+    L, pieces = int8_layer(E, H, I, seed=77)
+    xq, sx = tokens(1, H, seed=1)
+    ids = (torch.arange(T, device=DEV) % E).to(torch.int32)[:, None]
+    counts, offsets, sr, rp = moe.moe_permute(ids, E)
+    rows = moe.moe_grouped_ffn_w8a8(L, dev(xq).repeat(T, 1), dev(sx).repeat(T), k, counts, offsets, sr)
+    at = offsets.tolist()
+    for e in range(E):
+        row, tol = ref.ffn_row(xq[0], sx[0], *(p[e] for p in pieces))
+        assert np.all(np.abs(f64(rows[at[e]]) - row) <= tol)
+        assert bool((rows[at[e]:at[e + 1]] == rows[at[e]]).all())
+    no_device_error()
