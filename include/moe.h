@@ -350,7 +350,7 @@ MOE_API moe_status moe_linear_int8(const int8_t *xq, const float *sx, const int8
  *   rows[s] = s2 sh (Q2_e hq)
  * with exact integer sums, fp32 elsewhere.  h is quantised from its fp32 value, a
  * scale per row, so that its codes do not depend on a rounding in between; where h
- * holds a NaN (as a token's whose scale is one), sh and the whole row are NaN.  rows fp32 [T*k][H] in
+ * holds a NaN (as a token's whose scale is one) or an infinity, the whole row is NaN.  rows fp32 [T*k][H] in
  * sorted order for moe_combine or moe_combine_norm; rows past offsets[E] are not
  * written.  ws: at least moe_grouped_ffn_w8a8_workspace() bytes, 16-byte aligned;
  * calls that overlap on the GPU need a workspace each.  Slot tables as in
